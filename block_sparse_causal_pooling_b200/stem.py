@@ -37,6 +37,9 @@ STEM_SHARE_HEAD = 0
 STEM_SHARE_GROUP = 1
 STEM_SCORE_POOLED = 0
 STEM_SCORE_ANTIDIAG = 1
+STEM_KV_BF16 = 0
+STEM_KV_Q8 = 1
+STEM_KV_Q4 = 2
 
 
 class StemError(RuntimeError):
@@ -103,6 +106,28 @@ class stem_varlen_args_t(ctypes.Structure):
     ]
 
 
+class stem_cache_t(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_void_p), ("kbar", ctypes.c_void_p), ("vnorm", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("block", ctypes.c_int32), ("format", ctypes.c_int32), ("nseq", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32), ("vsum", ctypes.c_int32),
+    ]
+
+
+class stem_decode_args_t(ctypes.Structure):
+    _fields_ = [
+        ("cache", ctypes.POINTER(stem_cache_t)), ("q", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("budget", ctypes.c_void_p),
+        ("R", ctypes.c_int32), ("Hq", ctypes.c_int32), ("kcap", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("method", ctypes.POINTER(stem_method_t)),
+        ("sel_idx", ctypes.c_void_p), ("sel_cnt", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -111,6 +136,8 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     M = ctypes.POINTER(stem_method_t)
+    C, L = ctypes.POINTER(stem_cache_t), ctypes.POINTER(ctypes.c_int64)
+    A = ctypes.POINTER(stem_decode_args_t)
     sig = {
         "stem_prefill": (I, [P, P, P, I, I, I, I, I, I, F, F, I, P, P, P]),
         "stem_prefill_ex": (I, [ctypes.POINTER(stem_args_t), P]),
@@ -136,6 +163,13 @@ def _load() -> ctypes.CDLL:
         "stem_antidiag_m": (I, [P, P, I, I, I, I, I, I, I, M, P, P, Z, P, P]),
         "stem_select_p_m": (I, [P, P, I, I, I, I, M, P, P, P, P, Z, P]),
         "stem_varlen_workspace_size_m": (Z, [I, ctypes.POINTER(ctypes.c_int32), I, I, I, I, M]),
+        "stem_cache_page_bytes": (Z, [I, I, I]),
+        "stem_cache_append": (I, [C, P, P, I, I, L, P, P, P, P]),
+        "stem_cache_read": (I, [C, P, P, I, I, L, P, P, P, P]),
+        "stem_decode_workspace_size": (Z, [C, I, I, I]),
+        "stem_decode_select": (I, [A, P]),
+        "stem_decode_attn": (I, [A, P]),
+        "stem_decode": (I, [A, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -153,7 +187,9 @@ EXPORTED = ("stem_prefill", "stem_prefill_ex", "stem_prefill_host", "stem_budget
             "stem_pool_m", "stem_select_m", "stem_sparse_attn_m", "stem_prefill_varlen",
             "stem_varlen_workspace_size", "stem_varlen_sel_capacity", "stem_select_static",
             "stem_test_withhold_q", "stem_workspace_size_m", "stem_antidiag_m", "stem_select_p_m",
-            "stem_varlen_workspace_size_m")
+            "stem_varlen_workspace_size_m", "stem_cache_page_bytes", "stem_cache_append",
+            "stem_cache_read", "stem_decode_workspace_size", "stem_decode_select",
+            "stem_decode_attn", "stem_decode")
 
 
 def lib() -> ctypes.CDLL:

@@ -375,6 +375,142 @@ int stem_select_static(const float* qbar, const float* kbar, const float* vnorm,
                        int Hkv, int nb, int D, float rho_min, float tau, int k_min,
                        int32_t* sel_idx, int32_t* sel_cnt, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Decoding: attention of single query tokens over a paged cache of K and V. The paper describes
+ * prefill only; this is an interface addition that applies its block choice, one query token at a
+ * time, to the tokens after the prompt. A page of the cache is one selection block.
+ *
+ * Formats (stem_cache_t.format):
+ *   STEM_KV_BF16  K and V rows as bfloat16.
+ *   STEM_KV_Q8, STEM_KV_Q4  signed codes of 8 and 4 bits with a bfloat16 scale for every 32
+ *     channels of a row: with x those channels and Q = 127 or 7, s = bfloat16(max|x| / Q) and
+ *     c = clamp(rint(x / s), -Q, Q) (float32 quotients, ties to even; c = 0 where s = 0); the
+ *     row then stands for s * c. If one of the 32 is infinite or NaN, s is NaN and the 32
+ *     channels stand for NaN.
+ * Buffers of a cache:
+ *   pages  [num_pages, Hkv] records of stem_cache_page_bytes() bytes: block/16 tiles of 16 tokens,
+ *     each [K codes | V codes | scales]. Codes are unsigned with an offset of 8 (Q4) or 128 (Q8).
+ *     Codes lie in 32-bit little-endian words; word n of lane l is at byte
+ *     (n/4 * 32 + l) * 16 + n%4 * 4, with n = ((r/8) * (D/32) + d/32) * W + w for token r of the
+ *     tile and channel d, W = 1, 2, 4 words for Q4, Q8, BF16, and with x = d % 32:
+ *       K: l = (r%8) * 4 + x/8, e = x%8; Q4: w = 0, bits 16*(e%2) + 4*(e/2);
+ *          Q8: w = e/4, bits 16*(e%2) + 8*(e%4/2); BF16: w = e/2, bits 16*(e%2);
+ *       V: l = (x/4) * 4 + (r%8)/2, e = x%4; Q4: w = 0, bits 16*(r%2) + 4*e;
+ *          Q8: w = e/2, bits 16*(r%2) + 8*(e%2); BF16: w = e, bits 16*(r%2).
+ *     Scales (Q8, Q4): for each token D/32 bfloat16 of K, then D/32 of V.
+ *   kbar   [num_pages, Hkv, D] float32, vnorm [num_pages, Hkv] float32: mean K row and mean or
+ *     largest (vsum) V-row L2 norm of a full block, over the values that the cache stands for.
+ *     They are defined once the block's last token is written.
+ *   table  [nseq, max_blocks] int32: page of block j of sequence s; entries past a sequence's
+ *     blocks are not read. Sequences may share pages that neither of them writes.
+ * The caller owns the pages and hands them out; every device pointer belongs to the current device.
+ *
+ * Device-side checks: positions, lengths, sequence numbers, list entries and table entries are read
+ * on the device. One that is out of range sets the status word (if there is one) to STEM_ERR_ARG
+ * and what it names is left out: nothing outside the buffers is read or written.
+ * --------------------------------------------------------------------------------------- */
+#define STEM_KV_BF16 0
+#define STEM_KV_Q8 1
+#define STEM_KV_Q4 2
+
+typedef struct stem_cache {
+  void* pages;          /* 16-byte aligned */
+  float* kbar;          /* 16-byte aligned */
+  float* vnorm;
+  const int32_t* table;
+  int32_t num_pages, Hkv;
+  int32_t D, block;     /* 64 or 128 each */
+  int32_t format;
+  int32_t nseq;
+  int32_t max_blocks;   /* 1 .. STEM_MAX_NB */
+  int32_t vsum;         /* STEM_VSUM_MEAN or STEM_VSUM_MAX */
+} stem_cache_t;
+
+/* Bytes of one (page, kv head) record, 0 for an unsupported D, block or format. Host only. */
+size_t stem_cache_page_bytes(int D, int block, int format);
+
+/*
+ * Writes the K and V rows of new tokens: row (s, h, t) of k and v (device, dtype bfloat16 or
+ * float32; element ((s * strides[0]) + (h * strides[1]) + (t * strides[2]) + d, d contiguous) becomes
+ * token pos[s] + t of sequence s, for t < count[s] (NULL: T for every sequence). pos and count are
+ * device int32[nseq], 0 <= count[s] <= T. Strides are host values in elements, not negative, and
+ * multiples of 16 bytes. Each block whose last token is written gets its summaries; tokens of it
+ * that came earlier are read back from the page. Writing a position again replaces it, so a caller
+ * may take tokens back by appending at an earlier position. Two sequences of one call must not
+ * write the same page. status as in stem_args_t.
+ */
+int stem_cache_append(const stem_cache_t* c, const void* k, const void* v, int dtype, int T,
+                      const int64_t* strides, const int32_t* pos, const int32_t* count,
+                      int32_t* status, void* stream);
+
+/* The values that tokens pos[s] .. pos[s] + count[s] - 1 stand for, into k and v (rounded to
+ * bfloat16, or exact in float32). Arguments as
+ * for stem_cache_append; rows t >= count[s] are left as they were. */
+int stem_cache_read(const stem_cache_t* c, void* k, void* v, int dtype, int T,
+                    const int64_t* strides, const int32_t* pos, const int32_t* count,
+                    int32_t* status, void* stream);
+
+/*
+ * Arguments of a decode step: R query tokens ("rows"), each of one sequence of the cache. Several
+ * rows may belong to one sequence (draft tokens), each with its own number of visible tokens.
+ *   q [R, Hq, D], out [R, Hq, D]  bfloat16 (dtype STEM_F32 returns STEM_ERR_UNSUPPORTED)
+ *   lse [R, Hq] float32           optional: ln of the softmax denominator
+ *   rows [R] int32                sequence of each row; NULL: row r is sequence r (R <= nseq)
+ *   lens [R] int32                tokens that the row sees: 0 .. len - 1, its own K and V (appended
+ *                                 before) among them. 0: nothing is kept, out is 0, lse -infinity
+ *   budget [max_blocks] int32     k(i), as from stem_budget_m, on the device
+ *   kcap                          entries of a list, at least the largest k(i) in use; <= max_blocks
+ *   sel_idx [R, Hq, kcap], sel_cnt [R, Hq] int32   kept blocks of each row and head, ascending;
+ *                                 entries past sel_cnt are -1
+ *   method                        share, metric, beta, clamp (the schedule is in budget, the V
+ *                                 summary in the cache); score must be STEM_SCORE_POOLED
+ *   workspace                     stem_decode_workspace_size bytes, 256-byte aligned; calls that may
+ *                                 overlap on the device need one each
+ * All but the cache struct, method and sizes are read on the device: a captured graph may be replayed
+ * with new lens, table and page contents.
+ */
+typedef struct stem_decode_args {
+  const stem_cache_t* cache;
+  const void* q;
+  const int32_t* rows;
+  const int32_t* lens;
+  const int32_t* budget;
+  int32_t R, Hq, kcap, dtype;
+  const stem_method_t* method;
+  int32_t* sel_idx;
+  int32_t* sel_cnt;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* status;
+} stem_decode_args_t;
+
+/* Workspace bytes of the calls below, 0 for an invalid or empty request. Host only. */
+size_t stem_decode_workspace_size(const stem_cache_t* c, int R, int Hq, int kcap);
+
+/*
+ * The blocks each row keeps. With i = ceil(len / block) - 1 the row's own (diagonal) block and
+ * k = budget[i] (2 <= k <= i + 1 for i >= 1, 1 at i = 0):
+ *   s_hj = q_h . kbar_j / sqrt(D), j < i;  product: s_hj + ln n_j;  additive: s_hj + beta e_j
+ *   group share: ln n_j + ln sum_h softmax_{j < i}(s_h)_j, or sum_h s_hj + G beta e_j
+ *   kept = {0, i} and the k - 2 best of 1 .. i - 1, ties to the lower block; a key that is NaN
+ *   ranks last.
+ * Scores, metric and comparisons are double. out and lse are not used.
+ */
+int stem_decode_select(const stem_decode_args_t* a, void* stream);
+
+/*
+ * Softmax attention of each row over the tokens below lens of its kept blocks (sel_idx, sel_cnt:
+ * distinct blocks in [0, i], in any order; with STEM_SHARE_GROUP the list of a kv head's first
+ * query head serves all of them). 4- and 8-bit pages are read as they are: products of fp16
+ * weights and exact codes, float32 sums. budget is not used.
+ */
+int stem_decode_attn(const stem_decode_args_t* a, void* stream);
+
+/* stem_decode_select and stem_decode_attn as one call. */
+int stem_decode(const stem_decode_args_t* a, void* stream);
+
 /*
  * stem_test_withhold_q: TEST ONLY. With on != 0, later launches of the bfloat16 block-128
  * attention kernel (stem_prefill*, stem_sparse_attn*) skip each CTA's first Q tile, and later
