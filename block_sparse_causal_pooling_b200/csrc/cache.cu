@@ -3,7 +3,7 @@
 // Writing quantises each row once, as it arrives: with x the 32 channels of a group,
 //   s = bf16(max|x| / Q), c = clamp(rint(x / s), -Q, Q), the value it stands for is s * c.
 // s and x are bfloat16 (8 significant bits), so x / s is either a tie or at least 2^-17 away from
-// one, relative to its size: the float32 quotient (correctly rounded) gives the code that real
+// one, relative to its size: the correctly rounded float32 quotient gives the code that real
 // arithmetic gives. float32 inputs take the same float32 quotient as their definition.
 //
 // A block's summaries (kbar, vnorm) are computed by the call that writes its last token, from the
@@ -25,22 +25,38 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// Eight consecutive channels of one row, as float32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    x[2 * n] = __uint_as_float(w[n] << 16);
-    x[2 * n + 1] = __uint_as_float(w[n] & 0xffff0000u);
+// Eight consecutive channels of one row as they are in memory, and as float32.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = __ldcs(reinterpret_cast<const uint4*>(p));
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      x[2 * n] = __uint_as_float(w[n] << 16);
+      x[2 * n + 1] = __uint_as_float(w[n] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
 __device__ __forceinline__ uint32_t bf16_bits(float x) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
@@ -60,6 +76,13 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 // Quantises the 8 channels of this thread; the group's other channels are in the 3 neighbouring
 // lanes (a quad works on one row). x becomes the values that the codes stand for; code[] holds
 // offset codes (bfloat16 bits for the 16-bit format), the return value the scale's bits.
+//
+// The quotients are the correctly rounded ones without a division each (a division has a branch,
+// which would run the 8 of them one after another: 7 us a tile where this takes a fraction): with
+// r = 1/s correctly rounded, q0 = x r, e = x - q0 s (exact in an FMA) and q = q0 + e r is the
+// rounded x / s (Markstein's correction). Powers of two keep x and s away from the range's ends.
+// max|x| / Q is rounded once from the double product with 1/Q: 24 bits over 7 or 127 are never
+// nearer than 2^-32 to a float32 tie unless they are one.
 template <int FMT>
 __device__ __forceinline__ uint32_t quantise(float (&x)[8], uint32_t (&code)[8]) {
   if constexpr (FMT == STEM_KV_BF16) {
@@ -71,6 +94,8 @@ __device__ __forceinline__ uint32_t quantise(float (&x)[8], uint32_t (&code)[8])
     return 0;
   } else {
     using L = Kv<FMT, 128>;
+    constexpr float kTop = static_cast<float>(L::QMAX);
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
     // magnitudes as integers: ordered like the numbers, with infinity and NaN on top
     uint32_t top = 0;
 #pragma unroll
@@ -78,17 +103,21 @@ __device__ __forceinline__ uint32_t quantise(float (&x)[8], uint32_t (&code)[8])
     top = max(top, __shfl_xor_sync(kFull, top, 1));
     top = max(top, __shfl_xor_sync(kFull, top, 2));
     const bool finite = top < 0x7f800000u;
-    const uint32_t sb =
-        finite ? bf16_bits(__fdiv_rn(__uint_as_float(top), static_cast<float>(L::QMAX))) : 0x7fc0u;
+    const float largest = static_cast<float>(static_cast<double>(__uint_as_float(top)) *
+                                             (1.0 / static_cast<double>(L::QMAX)));
+    const uint32_t sb = finite ? bf16_bits(largest) : 0x7fc0u;
     const float s = bits_bf16(sb);
+    const float pow2 = s < 0x1p-60f ? 0x1p64f : s > 0x1p60f ? 0x1p-64f : 1.f;
+    const float ss = finite ? s * pow2 : 0.f;
+    const float r = s > 0.f && finite ? __frcp_rn(ss) : 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float c = 0.f;
-      if (finite && s > 0.f)
-        c = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -static_cast<float>(L::QMAX)),
-                  static_cast<float>(L::QMAX));
-      x[e] = s * c;  // exact (at most 8 + 7 significant bits); NaN for a group that is not finite
-      code[e] = static_cast<uint32_t>(static_cast<int>(c) + L::OFFSET);
+      const float y = finite ? x[e] * pow2 : 0.f;
+      const float q0 = y * r;
+      float q = fmaf(fmaf(-q0, ss, y), r, q0);
+      q = fminf(fmaxf(q, -kTop), kTop) + kMagic;
+      x[e] = s * (q - kMagic);  // exact (at most 8 + 7 bits); NaN for a group that is not finite
+      code[e] = __float_as_uint(q) - __float_as_uint(kMagic) + L::OFFSET;
     }
     return sb;
   }
@@ -221,101 +250,128 @@ struct Rows {
 };
 
 // The block this CTA works on: tokens [lo, hi) of its page. False: nothing to do.
+// `parts`: CTAs of a block.
 __device__ __forceinline__ bool my_block(const KvCache& c, const Rows& r, int& page, int& first,
-                                         int& lo, int& hi) {
+                                         int& lo, int& hi, int parts = 1) {
   const int seq = blockIdx.z;
   int j;
-  if (!kv_block_rows(c, r.pos[seq], r.count ? r.count[seq] : r.T, r.T, blockIdx.x, r.status, j,
-                     first, lo, hi))
+  if (!kv_block_rows(c, r.pos[seq], r.count ? r.count[seq] : r.T, r.T, blockIdx.x / parts,
+                     r.status, j, first, lo, hi))
     return false;
   page = kv_page(c, seq, j, r.status);
   return page >= 0;
 }
 
+constexpr int kThreads = 256;
+
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(8 * (D / 8)) append_kernel(KvCache c, Rows r, const T* k,
-                                                             const T* v) {
+__global__ void __launch_bounds__(kThreads) append_kernel(KvCache c, Rows r, const T* k,
+                                                          const T* v) {
   using L = Kv<FMT, D>;
-  constexpr int CH = D / 8;  // chunks of a row
+  constexpr int CH = D / 8;                    // chunks of a row
+  constexpr int SLOTS = kThreads / (8 * CH);  // tiles at a time
   int page, first, lo, hi;
   if (!my_block(c, r, page, first, lo, hi)) return;
-  const int head = blockIdx.y, pair = threadIdx.x / CH, chunk = threadIdx.x % CH;
+  const int head = blockIdx.y, slot = threadIdx.x / (8 * CH);
+  const int pair = threadIdx.x / CH % 8, chunk = threadIdx.x % CH;
   const Place<FMT, D> at(pair, chunk);
   unsigned char* rec = c.at(page, head);
   const int64_t base = static_cast<int64_t>(blockIdx.z) * r.s_seq +
                        static_cast<int64_t>(head) * r.s_head + chunk * 8;
   const bool done = hi == c.block;  // the block is complete: all of its tokens are summarised
   float ksum[8] = {0, 0, 0, 0, 0, 0, 0, 0}, vacc = 0.f;
-  for (int n = done ? 0 : lo / kKvTile; n <= (hi - 1) / kKvTile; ++n) {
+  const int n_end = (hi - 1) / kKvTile + 1;
+  // tiles of a thread are n0, n0 + SLOTS, ..: an order that depends on token positions alone
+  int n = (done ? 0 : lo / kKvTile) + slot;
+  Raw<T> rk[2], rv[2];
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int t = tile * kKvTile + 2 * pair + y;
+      if (t >= lo && t < hi) {
+        const int64_t o = base + static_cast<int64_t>(first + t) * r.s_tok;
+        rk[y].load(k + o);
+        rv[y].load(v + o);
+      } else {
+        rk[y].zero();
+        rv[y].zero();
+      }
+    }
+  };
+  fetch(n);
+  for (; n < n_end; n += SLOTS) {  // (a warp has one slot: n is uniform in it)
     unsigned char* tile = rec + static_cast<int64_t>(n) * L::TILE_BYTES;
     const int t0 = n * kKvTile + 2 * pair;
     bool fresh[2];
-    float xk[2][8] = {}, xv[2][8] = {};
-#pragma unroll
-    for (int y = 0; y < 2; ++y) fresh[y] = t0 + y >= lo && t0 + y < hi;
-    if (done && !(fresh[0] && fresh[1])) read_pair<FMT, D>(tile, at, xk, xv);
+    float xk[2][8], xv[2][8];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      if (fresh[y]) {
-        const int64_t o = base + static_cast<int64_t>(first + t0 + y) * r.s_tok;
-        load8(k + o, xk[y]);
-        load8(v + o, xv[y]);
-      }
+      fresh[y] = t0 + y >= lo && t0 + y < hi;
+      rk[y].get(xk[y]);
+      rv[y].get(xv[y]);
     }
-    uint32_t hv[2][2][4];
+    fetch(n + SLOTS);
+    if (__any_sync(kFull, fresh[0] || fresh[1])) {
+      uint32_t hv[2][2][4];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      // (every lane of a quad has the same tokens; the shuffles inside are warp-wide)
-      float nk[8], nv[8];
-      uint32_t ck[8], cv[8], kw[4];
+      for (int y = 0; y < 2; ++y) {
+        uint32_t ck[8], cv[8], kw[4];
+        const uint32_t sk = quantise<FMT>(xk[y], ck), sv = quantise<FMT>(xv[y], cv);
+        v_halves<FMT>(cv, hv[y][0]);
+        v_halves<FMT>(cv + 4, hv[y][1]);
+        if (fresh[y]) {
+          k_words<FMT>(ck, kw);
+          if constexpr (FMT == STEM_KV_BF16) {
+            *reinterpret_cast<uint4*>(tile + at.k(y, 0)) = make_uint4(kw[0], kw[1], kw[2], kw[3]);
+          } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) nk[e] = xk[y][e], nv[e] = xv[y][e];
-      const uint32_t sk = quantise<FMT>(nk, ck), sv = quantise<FMT>(nv, cv);
-      v_halves<FMT>(cv, hv[y][0]);
-      v_halves<FMT>(cv + 4, hv[y][1]);
-      if (fresh[y]) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xk[y][e] = nk[e], xv[y][e] = nv[e];
-        k_words<FMT>(ck, kw);
-        if constexpr (FMT == STEM_KV_BF16) {
-          *reinterpret_cast<uint4*>(tile + at.k(y, 0)) = make_uint4(kw[0], kw[1], kw[2], kw[3]);
-        } else {
-#pragma unroll
-          for (int w = 0; w < L::WPG; ++w)
-            *reinterpret_cast<uint32_t*>(tile + at.k(y, w)) = kw[w];
-          if (at.q == 0) {
-            unsigned char* row = tile + 2 * L::CODES + (2 * pair + y) * L::SCROW;
-            *reinterpret_cast<uint16_t*>(row + 2 * at.g) = static_cast<uint16_t>(sk);
-            *reinterpret_cast<uint16_t*>(row + 2 * (L::NG + at.g)) = static_cast<uint16_t>(sv);
+            for (int w = 0; w < L::WPG; ++w)
+              *reinterpret_cast<uint32_t*>(tile + at.k(y, w)) = kw[w];
+            if (at.q == 0) {
+              unsigned char* row = tile + 2 * L::CODES + (2 * pair + y) * L::SCROW;
+              *reinterpret_cast<uint16_t*>(row + 2 * at.g) = static_cast<uint16_t>(sk);
+              *reinterpret_cast<uint16_t*>(row + 2 * (L::NG + at.g)) = static_cast<uint16_t>(sv);
+            }
           }
         }
       }
-    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      unsigned char* dst = tile + L::CODES;
-      if (fresh[0] && fresh[1]) {
-        uint32_t w4[4];
+      for (int h = 0; h < 2; ++h) {
+        unsigned char* dst = tile + L::CODES;
+        if (fresh[0] && fresh[1]) {
+          uint32_t w4[4];
 #pragma unroll
-        for (int w = 0; w < L::WPG; ++w) w4[w] = hv[0][h][w] | hv[1][h][w] << 16;
-        if constexpr (FMT == STEM_KV_BF16) {
-          *reinterpret_cast<uint4*>(dst + at.v(h, 0)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-        } else {
-#pragma unroll
-          for (int w = 0; w < L::WPG; ++w) *reinterpret_cast<uint32_t*>(dst + at.v(h, w)) = w4[w];
-        }
-      } else {
-        // a lone token writes its halves and leaves the other token's as they are
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          if (fresh[y])
+          for (int w = 0; w < L::WPG; ++w) w4[w] = hv[0][h][w] | hv[1][h][w] << 16;
+          if constexpr (FMT == STEM_KV_BF16) {
+            *reinterpret_cast<uint4*>(dst + at.v(h, 0)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          } else {
 #pragma unroll
             for (int w = 0; w < L::WPG; ++w)
-              *reinterpret_cast<uint16_t*>(dst + at.v(h, w) + 2 * y) =
-                  static_cast<uint16_t>(hv[y][h][w]);
+              *reinterpret_cast<uint32_t*>(dst + at.v(h, w)) = w4[w];
+          }
+        } else {
+          // a lone token writes its halves and leaves the other token's as they are
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (fresh[y])
+#pragma unroll
+              for (int w = 0; w < L::WPG; ++w)
+                *reinterpret_cast<uint16_t*>(dst + at.v(h, w) + 2 * y) =
+                    static_cast<uint16_t>(hv[y][h][w]);
+        }
       }
     }
     if (done) {
+      if (!(fresh[0] && fresh[1])) {  // tokens that came with earlier calls
+        float ok[2][8], ov[2][8];
+        read_pair<FMT, D>(tile, at, ok, ov);
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (!fresh[y])
+#pragma unroll
+            for (int e = 0; e < 8; ++e) xk[y][e] = ok[y][e], xv[y][e] = ov[y][e];
+      }
+      __syncwarp();
       float sq[2] = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -338,50 +394,67 @@ __global__ void __launch_bounds__(8 * (D / 8)) append_kernel(KvCache c, Rows r, 
     }
   }
   if (!done) return;
-  // the eight pairs' sums, in a fixed order
-  __shared__ float ks[8][D];
-  __shared__ float vs[8];
+  // the sums of the slots' pairs, in a fixed order
+  constexpr int P = 8 * SLOTS;
+  __shared__ float ks[P][D];
+  __shared__ float vs[P];
+  const int part = slot * 8 + pair;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) ks[pair][chunk * 8 + e] = ksum[e];
-  if (chunk == 0) vs[pair] = vacc;
+  for (int e = 0; e < 8; e += 4)
+    *reinterpret_cast<float4*>(&ks[part][chunk * 8 + e]) =
+        make_float4(ksum[e], ksum[e + 1], ksum[e + 2], ksum[e + 3]);
+  if (chunk == 0) vs[part] = vacc;
   __syncthreads();
   const int64_t ph = static_cast<int64_t>(page) * c.Hkv + head;
-  for (int d = threadIdx.x; d < D; d += blockDim.x) {
-    const float s = ((ks[0][d] + ks[1][d]) + (ks[2][d] + ks[3][d])) +
-                    ((ks[4][d] + ks[5][d]) + (ks[6][d] + ks[7][d]));
-    c.kbar[ph * D + d] = s / static_cast<float>(c.block);
-  }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < D) {
+    const int d = threadIdx.x;
+    float s[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) s[i] = ks[i][d];
+#pragma unroll
+    for (int o = 1; o < P; o *= 2)
+#pragma unroll
+      for (int i = 0; i < P; i += 2 * o) s[i] += s[i + o];
+    c.kbar[ph * D + d] = s[0] / static_cast<float>(c.block);
+  } else if (threadIdx.x == D) {
     float s = vs[0];
-    for (int n = 1; n < 8; ++n) {
+    for (int i = 1; i < P; ++i) {
       if (c.vmax)
-        s = s > vs[n] || isnan(s) ? s : vs[n];
+        s = s > vs[i] || isnan(s) ? s : vs[i];
       else
-        s += vs[n];
+        s += vs[i];
     }
     c.vnorm[ph] = c.vmax ? s : s / static_cast<float>(c.block);
   }
 }
+
+// A CTA reads kReadTiles tiles, each thread its words of one tile at a time.
+constexpr int kReadTiles = 4;
 
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(8 * (D / 8)) read_kernel(KvCache c, Rows r, T* k, T* v) {
   using L = Kv<FMT, D>;
   constexpr int CH = D / 8;
   int page, first, lo, hi;
-  if (!my_block(c, r, page, first, lo, hi)) return;
+  const int parts = c.block / (kReadTiles * kKvTile);
+  if (!my_block(c, r, page, first, lo, hi, parts)) return;
   const int head = blockIdx.y, pair = threadIdx.x / CH, chunk = threadIdx.x % CH;
   const Place<FMT, D> at(pair, chunk);
   const unsigned char* rec = c.at(page, head);
   const int64_t base = static_cast<int64_t>(blockIdx.z) * r.s_seq +
                        static_cast<int64_t>(head) * r.s_head + chunk * 8;
-  for (int n = lo / kKvTile; n <= (hi - 1) / kKvTile; ++n) {
+  const int n0 = blockIdx.x % parts * kReadTiles;
+#pragma unroll
+  for (int i = 0; i < kReadTiles; ++i) {
+    const int t0 = (n0 + i) * kKvTile + 2 * pair;
+    const bool live[2] = {t0 >= lo && t0 < hi, t0 + 1 >= lo && t0 + 1 < hi};
+    if (!live[0] && !live[1]) continue;
     float xk[2][8], xv[2][8];
-    read_pair<FMT, D>(rec + static_cast<int64_t>(n) * L::TILE_BYTES, at, xk, xv);
+    read_pair<FMT, D>(rec + static_cast<int64_t>(n0 + i) * L::TILE_BYTES, at, xk, xv);
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      const int t = n * kKvTile + 2 * pair + y;
-      if (t < lo || t >= hi) continue;
-      const int64_t o = base + static_cast<int64_t>(first + t) * r.s_tok;
+      if (!live[y]) continue;
+      const int64_t o = base + static_cast<int64_t>(first + t0 + y) * r.s_tok;
       store8(k + o, xk[y]);
       store8(v + o, xv[y]);
     }
@@ -393,10 +466,11 @@ cudaError_t launch(bool write, const KvCache& c, const Rows& r, void* k, void* v
                    cudaStream_t st) {
   // blocks that T tokens can touch, from any offset in the first
   const unsigned nblk = static_cast<unsigned>((r.T + c.block - 2) / c.block + 1);
-  const dim3 grid(nblk, c.Hkv, c.nseq);
+  const unsigned parts = write ? 1 : c.block / (kReadTiles * kKvTile);
+  const dim3 grid(nblk * parts, c.Hkv, c.nseq);
   if (write)
-    append_kernel<FMT, D, T><<<grid, 8 * (D / 8), 0, st>>>(c, r, static_cast<const T*>(k),
-                                                           static_cast<const T*>(v));
+    append_kernel<FMT, D, T><<<grid, kThreads, 0, st>>>(c, r, static_cast<const T*>(k),
+                                                        static_cast<const T*>(v));
   else
     read_kernel<FMT, D, T><<<grid, 8 * (D / 8), 0, st>>>(c, r, static_cast<T*>(k),
                                                          static_cast<T*>(v));
