@@ -107,8 +107,8 @@ Layout layout(const stem_cache_t* c, int R, int Hq, int kcap) {
   L.partials = o;
   size_t part = 0;
   for (int share = 0; share < 2; ++share) {
-    const size_t n = decode_attn_partials(c->format, c->D, c->Hkv, c->max_blocks, R, Hq, kcap,
-                                          share != 0);
+    const size_t n = decode_attn_partials(c->format, c->D, c->block, c->Hkv, c->max_blocks, R, Hq,
+                                          kcap, share != 0);
     if (n > part) part = n;
   }
   o += align_up(sizeof(float) * part);

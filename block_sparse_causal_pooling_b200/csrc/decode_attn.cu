@@ -31,6 +31,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "decode_rows.cuh"
 
 namespace stem {
@@ -41,12 +43,23 @@ constexpr int kWarps = 4;
 constexpr int kHeadTile = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// A logit may exceed the running maximum by this much (in log2 units) before the accumulators are
+// rescaled: weights stay below 2^8, and most steps need neither the warp's maximum nor a rescale.
+constexpr float kSlack = 8.f;
+// The V scales' power of two puts the largest scale in [2^3, 2^4) when it is set, and is set again
+// when a scale exceeds 2^7 in its units: weights stay below 2^15, fp16's range.
+constexpr int kScaleSet = 3, kScaleSlack = 3;
 
 template <int FMT, int D>
 struct Cfg {
   using L = Kv<FMT, D>;
-  static constexpr int STAGES = FMT == STEM_KV_BF16 ? 3 : 4;
-  static constexpr int RING = STAGES * L::TILE_BYTES;  // a warp's
+  static constexpr bool Q = FMT != STEM_KV_BF16;
+  static constexpr int TPS = Q ? 2 : 1;  // tiles a warp takes at once
+  static constexpr int STAGES = FMT == STEM_KV_Q8 ? 2 : 3;
+  static constexpr int CTAS = FMT == STEM_KV_Q4 ? 4 : FMT == STEM_KV_Q8 ? 3 : 2;  // per SM, at least
+  static constexpr int STEP = kKvTile * TPS;                                      // tokens
+  static constexpr int STEP_BYTES = TPS * L::TILE_BYTES;
+  static constexpr int RING = STAGES * STEP_BYTES;  // a warp's
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -56,6 +69,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with the accumulator's first value given by column: D = A B + (c0, c1).
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], float c0, float c1, uint32_t a0,
+                                             uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -82,6 +105,11 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -101,15 +129,29 @@ struct Args {
   int splits;  // CTAs of an item
   __nv_bfloat16* out;
   float* lse;
-  float* part;  // [R][Hkv * head tiles][splits][8][D + 2]: numerator, max (log2 units), sum
+  // [R][Hkv * head tiles][splits][8] of each part of an item: statistics (max in log2 units, sum
+  // for the output, sum for lse) and [D] numerators
+  float4* stat;
+  float* part;
 };
 
-// The entries (block | heads << 16) of this CTA's part of its item's list.
-__device__ __forceinline__ int build_list(const Args& a, int row, int kv, int h0, int nh, int last,
-                                          uint32_t* ent, uint32_t* mask, uint32_t* wbuf) {
+// An entry of an item's list: the block's page, the block | query heads that keep it << 16.
+struct Entry {
+  int page;
+  uint32_t what;
+};
+__device__ __forceinline__ Entry entry_of(const Args& a, int seq, int j, uint32_t heads) {
+  const int page = kv_page(a.c, seq, j, a.r.status);
+  return page < 0 ? Entry{0, 0u} : Entry{page, static_cast<uint32_t>(j) | heads << 16};
+}
+
+// The entries of this CTA's part of its item's list; an invalid one has no heads.
+__device__ __forceinline__ int build_list(const Args& a, int row, int seq, int kv, int h0, int nh,
+                                          int last, Entry* ent, uint32_t* mask, uint32_t* wbuf) {
   const int tid = threadIdx.x, G = a.r.Hq / a.c.Hkv;
   const int e0 = blockIdx.x * a.chunk;
   const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G;
+  const uint32_t none = 0xffu << nh & 0xffu;  // columns without a head go along with any block
   if (a.share) {
     const int cnt = a.r.sel_cnt[head0];
     if ((cnt < 0 || cnt > a.r.kcap) && a.r.status) *a.r.status = STEM_ERR_ARG;
@@ -117,9 +159,12 @@ __device__ __forceinline__ int build_list(const Args& a, int row, int kv, int h0
     const int32_t* idx = a.r.sel_idx + head0 * a.r.kcap + e0;
     for (int e = tid; e < n; e += kWarps * 32) {
       const int j = idx[e];
-      const bool ok = j >= 0 && j <= last;
-      if (!ok && a.r.status) *a.r.status = STEM_ERR_ARG;
-      ent[e] = ok ? j | 0xff0000u : 0u;  // no heads: skipped
+      if (j >= 0 && j <= last) {
+        ent[e] = entry_of(a, seq, j, 0xffu);
+      } else {
+        if (a.r.status) *a.r.status = STEM_ERR_ARG;
+        ent[e] = Entry{0, 0u};
+      }
     }
     __syncthreads();
     return n;
@@ -164,7 +209,7 @@ __device__ __forceinline__ int build_list(const Args& a, int row, int kv, int h0
     for (int b = 0; b < 4; ++b) {
       const uint32_t m = mask[w] >> (8 * b) & 0xffu;
       if (!m) continue;
-      if (at >= 0 && at < a.chunk) ent[at] = (4 * w + b) | m << 16;
+      if (at >= 0 && at < a.chunk) ent[at] = entry_of(a, seq, 4 * w + b, m | none);
       ++at;
     }
   __syncthreads();
@@ -172,89 +217,107 @@ __device__ __forceinline__ int build_list(const Args& a, int row, int kv, int h0
 }
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_kernel(const Args a) {
+__global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(const Args a) {
   using L = Kv<FMT, D>;
   using C = Cfg<FMT, D>;
-  constexpr bool kQuant = FMT != STEM_KV_BF16;
-  constexpr int NG = L::NG;
+  constexpr bool kQuant = C::Q;
+  constexpr int NG = L::NG, TPS = C::TPS;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t wbuf[kWarps];
-  __shared__ float s_m[kWarps][kHeadTile], s_l[kWarps][kHeadTile];
-  uint32_t* ent = reinterpret_cast<uint32_t*>(smem + kWarps * C::RING);
-  uint32_t* mask = ent + a.chunk;
+  __shared__ float s_m[kWarps][kHeadTile], s_l[kWarps][kHeadTile], s_x[kWarps][kHeadTile];
+  Entry* ent = reinterpret_cast<Entry*>(smem + kWarps * C::RING);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(ent + a.chunk);
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int G = a.r.Hq / a.c.Hkv, tiles_h = (G + kHeadTile - 1) / kHeadTile;
   const int row = blockIdx.z, kv = blockIdx.y / tiles_h, h0 = blockIdx.y % tiles_h * kHeadTile;
   const int nh = min(G - h0, kHeadTile);
+  const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
   int seq, len;
   decode_row(a.c, a.r, row, seq, len);
   const int last = (len + a.c.block - 1) / a.c.block - 1;
-  const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
-
-  const int n_ent = last >= 0 ? build_list(a, row, kv, h0, nh, last, ent, mask, wbuf) : 0;
 
   // ---- the queries, as B operands: head g, channels 8t .. 8t + 7 of each group
   uint32_t qf[NG][4];
-  float qscale = kLog2e / sqrtf(static_cast<float>(D));  // of head g: logits in log2 units
-  float cinit[NG][2];
   {
-    const bool on = g < nh;
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.r.q) +
-                                                    (head0 + (on ? g : 0)) * D + 8 * t);
+                                                    (head0 + (g < nh ? g : 0)) * D + 8 * t);
 #pragma unroll
     for (int y = 0; y < NG; ++y) {
-      const uint4 u = on ? p[y * (kKvGroup / 8)] : make_uint4(0, 0, 0, 0);
+      const uint4 u = g < nh ? p[y * (kKvGroup / 8)] : make_uint4(0, 0, 0, 0);
       qf[y][0] = u.x, qf[y][1] = u.y, qf[y][2] = u.z, qf[y][3] = u.w;
     }
-    if constexpr (kQuant) {
-      uint32_t top = 0;
+  }
+  const int n_ent = last >= 0 ? build_list(a, row, seq, kv, h0, nh, last, ent, mask, wbuf) : 0;
+
+  float* o_s = reinterpret_cast<float*>(smem);  // [kWarps][8][D], over the rings at the end
+  const int64_t item = (static_cast<int64_t>(row) * gridDim.y + blockIdx.y) * a.splits + blockIdx.x;
+  if (n_ent == 0) {  // nothing here
+    if (a.splits > 1) {
+      if (tid < kHeadTile) a.stat[item * kHeadTile + tid] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    } else {
+      for (int n = tid; n < nh * D; n += kWarps * 32) a.out[head0 * D + n] = __float2bfloat16_rn(0.f);
+      if (tid < nh && a.lse) a.lse[head0 + tid] = -INFINITY;
+    }
+    return;
+  }
+
+  float qscale = kLog2e / sqrtf(static_cast<float>(D));  // of head g: logits in log2 units
+  float cinit[NG][2];
+  if constexpr (kQuant) {
+    uint32_t top = 0;
 #pragma unroll
-      for (int y = 0; y < NG; ++y)
+    for (int y = 0; y < NG; ++y)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          top = max(top, max(qf[y][n] & 0x7fffu, qf[y][n] >> 16 & 0x7fffu));
-      top = max(top, __shfl_xor_sync(kFull, top, 1));
-      top = max(top, __shfl_xor_sync(kFull, top, 2));
-      // exponent that brings the largest |q| to [2^14, 2^15); at least -100, so that what undoes
-      // it stays a float32
-      const int up = top < 0x0080u || top >= 0x7f80u
-                         ? 0
-                         : max(14 - (static_cast<int>(top >> 7) - 127), -100);
-      qscale *= ldexpf(1.f, min(24 - up, 126));
+      for (int n = 0; n < 4; ++n)
+        top = max(top, max(qf[y][n] & 0x7fffu, qf[y][n] >> 16 & 0x7fffu));
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+    // exponent that brings the largest |q| to [2^14, 2^15); at least -100, so that what undoes it
+    // stays a float32
+    const int up = top < 0x0080u || top >= 0x7f80u
+                       ? 0
+                       : max(14 - (static_cast<int>(top >> 7) - 127), -100);
+    qscale *= ldexpf(1.f, min(24 - up, 126));
+    const float up1 = ldexpf(1.f, up / 2), up2 = ldexpf(1.f, up - up / 2);
 #pragma unroll
-      for (int y = 0; y < NG; ++y) {
-        float sum = 0.f;
+    for (int y = 0; y < NG; ++y) {
+      float sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const __half2 h = __floats2half2_rn(ldexpf(low16(qf[y][n]), up),
-                                              ldexpf(high16(qf[y][n]), up));
-          sum += __low2float(h) + __high2float(h);
-          // odd words meet upper nibbles, which weigh 16 times as much
-          const __half2 w = FMT == STEM_KV_Q4 && (n & 1)
-                                ? __hmul2(h, __floats2half2_rn(0.0625f, 0.0625f))
-                                : h;
-          qf[y][n] = *reinterpret_cast<const uint32_t*>(&w);
-        }
-        sum += __shfl_xor_sync(kFull, sum, 1);
-        sum += __shfl_xor_sync(kFull, sum, 2);
-        sum *= -static_cast<float>(L::OFFSET) * 0x1p-24f;
-        cinit[y][0] = __shfl_sync(kFull, sum, 8 * t);      // head 2t: lane row 2t
-        cinit[y][1] = __shfl_sync(kFull, sum, 8 * t + 4);  // head 2t + 1
+      for (int n = 0; n < 4; ++n) {
+        const __half2 h = __floats2half2_rn(low16(qf[y][n]) * up1 * up2,
+                                            high16(qf[y][n]) * up1 * up2);
+        sum += __low2float(h) + __high2float(h);
+        // odd words meet upper nibbles, which weigh 16 times as much
+        const __half2 w = FMT == STEM_KV_Q4 && (n & 1)
+                              ? __hmul2(h, __floats2half2_rn(0.0625f, 0.0625f))
+                              : h;
+        qf[y][n] = *reinterpret_cast<const uint32_t*>(&w);
       }
+      sum += __shfl_xor_sync(kFull, sum, 1);
+      sum += __shfl_xor_sync(kFull, sum, 2);
+      sum *= -static_cast<float>(L::OFFSET) * 0x1p-24f;
+      cinit[y][0] = __shfl_sync(kFull, sum, 8 * t);      // head 2t: lane row 2t
+      cinit[y][1] = __shfl_sync(kFull, sum, 8 * t + 4);  // head 2t + 1
     }
   }
   const float qs0 = __shfl_sync(kFull, qscale, 8 * t), qs1 = __shfl_sync(kFull, qscale, 8 * t + 4);
 
   float acc[2 * NG][4];  // rows: channels; columns: heads 2t, 2t + 1
   float asum[4];         // row y: sum of group y's weights
-  float m0, m1, l0, l1, vf;
+  float m0, m1, l0, l1;  // running maximum (log2 units) and sum of the weights as the MMA sees them
+  float x0, x1;          // at 16 bits: sum of the weights before rounding
+  float vf;              // power of two of the V scales
+  int vlim;              // largest scale (bf16 bits) that vf is good for
   unsigned char* ring = smem + warp * C::RING;
-  const int tpb = a.c.block / kKvTile;
-  const int units = n_ent * tpb;
-  bool odd = false;  // a column's result is not a number
+  const int spb_log = a.c.block / C::STEP == 2 ? 1 : a.c.block / C::STEP == 4 ? 2 : 3;
+  const int units = n_ent << spb_log;
+  const int64_t page_bytes = static_cast<int64_t>(a.c.Hkv) * a.c.record;
+  const unsigned char* head_pages = a.c.at(0, kv) + lane * 16;
 
-  // Streams the tiles of the entries that one of `heads` keeps.
+  // Streams the steps of the entries that one of `heads` keeps.
   auto stream = [&](uint32_t heads) {
 #pragma unroll
     for (int n = 0; n < 2 * NG; ++n)
@@ -263,29 +326,27 @@ __global__ void __launch_bounds__(kWarps * 32) attn_kernel(const Args a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) asum[e] = 0.f;
     m0 = m1 = -INFINITY;
-    l0 = l1 = 0.f;
-    vf = 0x1p126f;
+    l0 = l1 = x0 = x1 = 0.f;
+    vf = 1.f;
+    vlim = -1;
 
-    // tokens of unit u, 0 where there is nothing to do
-    auto tokens = [&](int u, uint32_t& e) -> int {
-      if (u >= units) return 0;
-      e = ent[u / tpb];
-      if (!(e >> 16 & heads)) return 0;
-      const int j = e & 0xffffu;
-      return min(max(len - j * a.c.block - u % tpb * kKvTile, 0), kKvTile);
+    // tokens of step u that are there, 0 or less where there is nothing to do
+    auto tokens = [&](int u, const Entry& e) -> int {
+      if (!(e.what >> 16 & heads)) return 0;
+      return len - static_cast<int>(e.what & 0xffffu) * a.c.block -
+             (u & ((1 << spb_log) - 1)) * C::STEP;
     };
     auto fetch = [&](int u, int stage) {
-      uint32_t e = 0;
-      if (tokens(u, e) > 0) {
-        const int page = kv_page(a.c, seq, e & 0xffffu, a.r.status);
-        if (page >= 0) {
+      if (u < units) {
+        const Entry e = ent[u >> spb_log];
+        if (tokens(u, e) > 0) {
           const unsigned char* src =
-              a.c.at(page, kv) + static_cast<int64_t>(u % tpb) * L::TILE_BYTES + lane * 16;
-          unsigned char* dst = ring + stage * L::TILE_BYTES + lane * 16;
+              head_pages + e.page * page_bytes + (u & ((1 << spb_log) - 1)) * C::STEP_BYTES;
+          unsigned char* dst = ring + stage * C::STEP_BYTES + lane * 16;
 #pragma unroll
-          for (int n = 0; n < L::TILE_BYTES / 512; ++n) cp16(dst + n * 512, src + n * 512);
-          if (lane < L::TILE_BYTES % 512 / 16)
-            cp16(dst + L::TILE_BYTES / 512 * 512, src + L::TILE_BYTES / 512 * 512);
+          for (int n = 0; n < C::STEP_BYTES / 512; ++n) cp16(dst + n * 512, src + n * 512);
+          if (C::STEP_BYTES % 512 != 0 && lane < C::STEP_BYTES % 512 / 16)
+            cp16(dst + C::STEP_BYTES / 512 * 512, src + C::STEP_BYTES / 512 * 512);
         }
       }
       cp_commit();
@@ -294,114 +355,149 @@ __global__ void __launch_bounds__(kWarps * 32) attn_kernel(const Args a) {
     for (int n = 0; n < C::STAGES - 1; ++n) fetch(warp + n * kWarps, n);
     int stage = 0;
     for (int u = warp; u < units; u += kWarps) {
-      cp_wait<C::STAGES - 2>();
+      // the next step to fetch takes the stage that the step before this one has left
+      fetch(u + (C::STAGES - 1) * kWarps, stage == 0 ? C::STAGES - 1 : stage - 1);
+      cp_wait<C::STAGES - 1>();
       __syncwarp();
-      uint32_t e = 0;
-      int valid = tokens(u, e);
-      if (valid > 0 && kv_page(a.c, seq, e & 0xffffu, a.r.status) < 0) valid = 0;
+      const Entry e = ent[u >> spb_log];
+      const int valid = tokens(u, e);
       if (valid > 0) {
-        const unsigned char* tile = ring + stage * L::TILE_BYTES;
-        // ---- logits: rows are tokens g and g + 8, columns heads 2t and 2t + 1
-        float z[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t sv[2][2];  // V scales of tokens g, g + 8: two groups a word
-        if constexpr (!kQuant) {
+        const unsigned char* step = ring + stage * C::STEP_BYTES;
+        // ---- logits: rows are tokens g and g + 8 of a tile, columns heads 2t and 2t + 1
+        float z[TPS][4];
+        uint32_t sv[TPS][2][2];  // V scales of tokens g, g + 8: two groups a word
 #pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            const uint4 ka = *reinterpret_cast<const uint4*>(tile + L::word(0, y, 0, lane));
-            const uint4 kb = *reinterpret_cast<const uint4*>(tile + L::word(1, y, 0, lane));
-            mma_bf16(z, ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
-            mma_bf16(z, ka.z, kb.z, ka.w, kb.w, qf[y][2], qf[y][3]);
-          }
-        } else {
-          uint32_t kw[2][NG * L::WPG], sk[2][2];
+        for (int i = 0; i < TPS; ++i) {
+          const unsigned char* tile = step + i * L::TILE_BYTES;
 #pragma unroll
-          for (int p = 0; p < L::PIECES; ++p) {
-            const uint4 x = *reinterpret_cast<const uint4*>(tile + p * 512 + lane * 16);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          for (int n = 0; n < 4; ++n) z[i][n] = 0.f;
+          if constexpr (!kQuant) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-              kw[(p * 4 + n) / (NG * L::WPG)][(p * 4 + n) % (NG * L::WPG)] = w[n];
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const unsigned char* s = tile + 2 * L::CODES + (g + 8 * i) * L::SCROW;
-            if constexpr (NG == 4) {
-              const uint4 x = *reinterpret_cast<const uint4*>(s);
-              sk[i][0] = x.x, sk[i][1] = x.y, sv[i][0] = x.z, sv[i][1] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(s);
-              sk[i][0] = x.x, sv[i][0] = x.y;
-              sk[i][1] = sv[i][1] = 0;
+            for (int y = 0; y < NG; ++y) {
+              const uint4 ka = *reinterpret_cast<const uint4*>(tile + L::word(0, y, 0, lane));
+              const uint4 kb = *reinterpret_cast<const uint4*>(tile + L::word(1, y, 0, lane));
+              mma_bf16(z[i], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
+              mma_bf16(z[i], ka.z, kb.z, ka.w, kb.w, qf[y][2], qf[y][3]);
             }
-          }
+          } else {
+            uint32_t kw[2][NG * L::WPG], sk[2][2];
 #pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            float d[4] = {cinit[y][0], cinit[y][1], cinit[y][0], cinit[y][1]};
-            if constexpr (FMT == STEM_KV_Q4) {
-              const uint32_t a0 = kw[0][y], a1 = kw[1][y];
-              mma_f16(d, a0 & 0x000f000fu, a1 & 0x000f000fu, a0 & 0x00f000f0u, a1 & 0x00f000f0u,
-                      qf[y][0], qf[y][1]);
-              mma_f16(d, a0 >> 8 & 0x000f000fu, a1 >> 8 & 0x000f000fu, a0 >> 8 & 0x00f000f0u,
-                      a1 >> 8 & 0x00f000f0u, qf[y][2], qf[y][3]);
-            } else {
+            for (int p = 0; p < L::PIECES; ++p) {
+              const uint4 x = *reinterpret_cast<const uint4*>(tile + p * 512 + lane * 16);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const uint32_t a0 = kw[0][2 * y + w], a1 = kw[1][2 * y + w];
-                mma_f16(d, a0 & 0x00ff00ffu, a1 & 0x00ff00ffu, a0 >> 8 & 0x00ff00ffu,
-                        a1 >> 8 & 0x00ff00ffu, qf[y][2 * w], qf[y][2 * w + 1]);
+              for (int n = 0; n < 4; ++n)
+                kw[(p * 4 + n) / (NG * L::WPG)][(p * 4 + n) % (NG * L::WPG)] = w[n];
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const unsigned char* s = tile + 2 * L::CODES + (g + 8 * r) * L::SCROW;
+              if constexpr (NG == 4) {
+                const uint4 x = *reinterpret_cast<const uint4*>(s);
+                sk[r][0] = x.x, sk[r][1] = x.y, sv[i][r][0] = x.z, sv[i][r][1] = x.w;
+              } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(s);
+                sk[r][0] = x.x, sv[i][r][0] = x.y;
+                sk[r][1] = sv[i][r][1] = 0;
               }
             }
-            const float s0 = y & 1 ? high16(sk[0][y / 2]) : low16(sk[0][y / 2]);
-            const float s1 = y & 1 ? high16(sk[1][y / 2]) : low16(sk[1][y / 2]);
-            z[0] = fmaf(s0, d[0], z[0]);
-            z[1] = fmaf(s0, d[1], z[1]);
-            z[2] = fmaf(s1, d[2], z[2]);
-            z[3] = fmaf(s1, d[3], z[3]);
-          }
-        }
-        // ---- running softmax; tokens past the row's length and heads that do not keep the block
-        // get weight 0 whatever their bytes hold
-        const uint32_t hb = e >> 16 & heads;
-        const bool on0 = hb >> (2 * t) & 1, on1 = hb >> (2 * t + 1) & 1;
-        const bool lo = g < valid, hi = g + 8 < valid;
-        z[0] = lo && on0 ? z[0] * qs0 : -INFINITY;
-        z[1] = lo && on1 ? z[1] * qs1 : -INFINITY;
-        z[2] = hi && on0 ? z[2] * qs0 : -INFINITY;
-        z[3] = hi && on1 ? z[3] * qs1 : -INFINITY;
-        float n0 = fmaxf(z[0], z[2]), n1 = fmaxf(z[1], z[3]);
 #pragma unroll
-        for (int o = 4; o < 32; o *= 2) {
-          n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, o));
-          n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, o));
-        }
-        n0 = fmaxf(n0, m0);
-        n1 = fmaxf(n1, m1);
-        const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-        float up = 1.f;  // change of the weights' power of two
-        if constexpr (kQuant) {
-          // largest finite V scale of the tile: bf16 bits order like the numbers
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (i == 0 ? !lo : !hi) sv[i][0] = sv[i][1] = 0;
-#pragma unroll
-            for (int w = 0; w < NG / 2; ++w) {
-              const uint32_t x = sv[i][w] & 0xffffu, y = sv[i][w] >> 16;
-              top = max(top, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
+            for (int y = 0; y < NG; ++y) {
+              float d[4];
+              if constexpr (FMT == STEM_KV_Q4) {
+                const uint32_t a0 = kw[0][y], a1 = kw[1][y];
+                mma_f16_from(d, cinit[y][0], cinit[y][1], a0 & 0x000f000fu, a1 & 0x000f000fu,
+                             a0 & 0x00f000f0u, a1 & 0x00f000f0u, qf[y][0], qf[y][1]);
+                mma_f16(d, a0 >> 8 & 0x000f000fu, a1 >> 8 & 0x000f000fu, a0 >> 8 & 0x00f000f0u,
+                        a1 >> 8 & 0x00f000f0u, qf[y][2], qf[y][3]);
+              } else {
+                const uint32_t a0 = kw[0][2 * y], a1 = kw[1][2 * y];
+                const uint32_t b0 = kw[0][2 * y + 1], b1 = kw[1][2 * y + 1];
+                mma_f16_from(d, cinit[y][0], cinit[y][1], a0 & 0x00ff00ffu, a1 & 0x00ff00ffu,
+                             a0 >> 8 & 0x00ff00ffu, a1 >> 8 & 0x00ff00ffu, qf[y][0], qf[y][1]);
+                mma_f16(d, b0 & 0x00ff00ffu, b1 & 0x00ff00ffu, b0 >> 8 & 0x00ff00ffu,
+                        b1 >> 8 & 0x00ff00ffu, qf[y][2], qf[y][3]);
+              }
+              const float s0 = y & 1 ? high16(sk[0][y / 2]) : low16(sk[0][y / 2]);
+              const float s1 = y & 1 ? high16(sk[1][y / 2]) : low16(sk[1][y / 2]);
+              z[i][0] = fmaf(s0, d[0], z[i][0]);
+              z[i][1] = fmaf(s0, d[1], z[i][1]);
+              z[i][2] = fmaf(s1, d[2], z[i][2]);
+              z[i][3] = fmaf(s1, d[3], z[i][3]);
             }
           }
-          top = __reduce_max_sync(kFull, top);
-          const float f = __uint_as_float(min(267u - (top >> 7), 253u) << 23);
-          if (f < vf) {
-            up = f / vf;
-            vf = f;
-          }
+#pragma unroll
+          for (int n = 0; n < 4; ++n) z[i][n] *= n & 1 ? qs1 : qs0;
         }
-        if (__any_sync(kFull, n0 != m0 || n1 != m1 || up != 1.f)) {
-          const float a0 = exp2f(m0 - b0), a1 = exp2f(m1 - b1);
+        // ---- tokens past the row's length and heads that do not keep the block: weight 0, and
+        // scale 0, whatever their bytes hold
+        const uint32_t hb = e.what >> 16 & heads;
+        if (valid < C::STEP || hb != 0xffu) {
+          const bool on0 = hb >> (2 * t) & 1, on1 = hb >> (2 * t + 1) & 1;
+#pragma unroll
+          for (int i = 0; i < TPS; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const bool in = i * kKvTile + 8 * r + g < valid;
+              if (!(in && on0)) z[i][2 * r] = -INFINITY;
+              if (!(in && on1)) z[i][2 * r + 1] = -INFINITY;
+              if (kQuant && !in) sv[i][r][0] = sv[i][r][1] = 0;
+            }
+        }
+        // ---- running maximum and scale: exact only when a logit or a scale leaves its slack
+        float n0 = fmaxf(z[0][0], z[0][2]), n1 = fmaxf(z[0][1], z[0][3]);
+        bool move = false;
+        if constexpr (kQuant) {
+          n0 = fmaxf(n0, fmaxf(z[1][0], z[1][2]));
+          n1 = fmaxf(n1, fmaxf(z[1][1], z[1][3]));
+          uint32_t top = __vmaxu2(__vmaxu2(sv[0][0][0], sv[0][1][0]),
+                                  __vmaxu2(sv[1][0][0], sv[1][1][0]));
+          if constexpr (NG == 4)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(sv[0][0][1], sv[0][1][1]),
+                                         __vmaxu2(sv[1][0][1], sv[1][1][1])));
+          move = static_cast<int>(max(top & 0xffffu, top >> 16)) > vlim;
+        }
+        move |= n0 > m0 + kSlack || n1 > m1 + kSlack;
+        if (__any_sync(kFull, move)) {
+#pragma unroll
+          for (int o = 4; o < 32; o *= 2) {
+            n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, o));
+            n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, o));
+          }
+          n0 = fmaxf(n0, m0);
+          n1 = fmaxf(n1, m1);
+          const float a0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+          const float a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+          m0 = n0;
+          m1 = n1;
           l0 *= a0;
           l1 *= a1;
-          const float c0 = a0 * up, c1 = a1 * up;
+          x0 *= a0;
+          x1 *= a1;
+          float c0 = a0, c1 = a1;
+          if constexpr (kQuant) {
+            uint32_t top = 0;  // largest finite scale: bf16 bits order like the numbers
+#pragma unroll
+            for (int i = 0; i < TPS; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int w = 0; w < NG / 2; ++w) {
+                  const uint32_t lo = sv[i][r][w] & 0xffffu, hi = sv[i][r][w] >> 16;
+                  top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                }
+            top = __reduce_max_sync(kFull, top);
+            if (static_cast<int>(top) > vlim) {
+              const uint32_t ex = top >> 7;  // biased exponent
+              const float f = __uint_as_float(min(254u + kScaleSet - ex, 245u) << 23);
+              if (vlim >= 0) {
+                c0 *= f / vf;
+                c1 *= f / vf;
+              }
+              vf = f;
+              vlim = static_cast<int>((ex + kScaleSlack + 1) << 7) - 1;
+            }
+          }
 #pragma unroll
           for (int n = 0; n < 2 * NG; ++n) {
             acc[n][0] *= c0;
@@ -413,75 +509,83 @@ __global__ void __launch_bounds__(kWarps * 32) attn_kernel(const Args a) {
           asum[1] *= c1;
           asum[2] *= c0;
           asum[3] *= c1;
-          m0 = n0;
-          m1 = n1;
         }
-        float p[4] = {exp2f(z[0] - b0), exp2f(z[1] - b1), exp2f(z[2] - b0), exp2f(z[3] - b1)};
-        const unsigned char* vt = tile + L::CODES;
-        if constexpr (!kQuant) {
-          const uint32_t pa = pack_bf16(p[0], p[1]), pb = pack_bf16(p[2], p[3]);
-          l0 += low16(pa) + low16(pb);
-          l1 += high16(pa) + high16(pb);
-          const uint32_t w0 = transpose8(pa), w1 = transpose8(pb);
-          // V rows of tokens that are not there may hold anything: 0 * NaN is not 0
-          uint32_t keep0 = kFull, keep1 = kFull;
-          if (valid < kKvTile) {
-            keep0 = (2 * t < valid ? 0xffffu : 0u) | (2 * t + 1 < valid ? 0xffff0000u : 0u);
-            keep1 = (2 * t + 8 < valid ? 0xffffu : 0u) | (2 * t + 9 < valid ? 0xffff0000u : 0u);
-          }
+        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
-            uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
-            if (valid < kKvTile) {
-              va.x &= keep0, va.y &= keep0, va.z &= keep0, va.w &= keep0;
-              vb.x &= keep1, vb.y &= keep1, vb.z &= keep1, vb.w &= keep1;
-            }
-            mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, w0, w1);
-            mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, w0, w1);
-          }
-        } else {
-          l0 += p[0] + p[2];
-          l1 += p[1] + p[3];
+        for (int i = 0; i < TPS; ++i) {
+          float p[4] = {ex2(z[i][0] - b0), ex2(z[i][1] - b1), ex2(z[i][2] - b0),
+                        ex2(z[i][3] - b1)};
+          const unsigned char* vt = step + i * L::TILE_BYTES + L::CODES;
+          if constexpr (!kQuant) {
+            x0 += p[0] + p[2];
+            x1 += p[1] + p[3];
+            const uint32_t pa = pack_bf16(p[0], p[1]), pb = pack_bf16(p[2], p[3]);
+            l0 += low16(pa) + low16(pb);
+            l1 += high16(pa) + high16(pb);
+            const uint32_t w0 = transpose8(pa), w1 = transpose8(pb);
+            if (valid >= kKvTile) {
 #pragma unroll
-          for (int n = 0; n < 4; ++n) p[n] *= vf;
-          uint32_t vw[2][NG * L::WPG];
-#pragma unroll
-          for (int q = 0; q < L::PIECES; ++q) {
-            const uint4 x = *reinterpret_cast<const uint4*>(vt + q * 512 + lane * 16);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-              vw[(q * 4 + n) / (NG * L::WPG)][(q * 4 + n) % (NG * L::WPG)] = w[n];
-          }
-#pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            const float s0 = y & 1 ? high16(sv[0][y / 2]) : low16(sv[0][y / 2]);
-            const float s1 = y & 1 ? high16(sv[1][y / 2]) : low16(sv[1][y / 2]);
-            // (a head that does not keep the block has weight 0 even where the scale is NaN)
-            const uint32_t w0 = transpose8(pack_f16(on0 ? p[0] * s0 : 0.f, on1 ? p[1] * s0 : 0.f));
-            const uint32_t w1 = transpose8(pack_f16(on0 ? p[2] * s1 : 0.f, on1 ? p[3] * s1 : 0.f));
-            const uint32_t one = g == y ? 0x3c003c00u : 0u;
-            mma_f16(asum, one, 0u, one, 0u, w0, w1);
-            if constexpr (FMT == STEM_KV_Q4) {
-              const uint32_t va = vw[0][y], vb = vw[1][y];
-              mma_f16(acc[2 * y], va & 0x000f000fu, va & 0x00f000f0u, vb & 0x000f000fu,
-                      vb & 0x00f000f0u, w0, w1);
-              mma_f16(acc[2 * y + 1], va >> 8 & 0x000f000fu, va >> 8 & 0x00f000f0u,
-                      vb >> 8 & 0x000f000fu, vb >> 8 & 0x00f000f0u, w0, w1);
+              for (int y = 0; y < NG; ++y) {
+                const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
+                const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
+                mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, w0, w1);
+                mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, w0, w1);
+              }
             } else {
+              // V rows of tokens that are not there may hold anything: 0 * NaN is not 0
+              const uint32_t ka = (2 * t < valid ? 0xffffu : 0u) |
+                                  (2 * t + 1 < valid ? 0xffff0000u : 0u);
+              const uint32_t kb = (2 * t + 8 < valid ? 0xffffu : 0u) |
+                                  (2 * t + 9 < valid ? 0xffff0000u : 0u);
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t va = vw[0][2 * y + x], vb = vw[1][2 * y + x];
-                mma_f16(acc[2 * y + x], va & 0x00ff00ffu, va >> 8 & 0x00ff00ffu,
-                        vb & 0x00ff00ffu, vb >> 8 & 0x00ff00ffu, w0, w1);
+              for (int y = 0; y < NG; ++y) {
+                const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
+                const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
+                mma_bf16(acc[2 * y], va.x & ka, va.y & ka, vb.x & kb, vb.y & kb, w0, w1);
+                mma_bf16(acc[2 * y + 1], va.z & ka, va.w & ka, vb.z & kb, vb.w & kb, w0, w1);
+              }
+            }
+          } else {
+            l0 += p[0] + p[2];
+            l1 += p[1] + p[3];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) p[n] *= vf;
+            uint32_t vw[2][NG * L::WPG];
+#pragma unroll
+            for (int q = 0; q < L::PIECES; ++q) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vt + q * 512 + lane * 16);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                vw[(q * 4 + n) / (NG * L::WPG)][(q * 4 + n) % (NG * L::WPG)] = w[n];
+            }
+#pragma unroll
+            for (int y = 0; y < NG; ++y) {
+              const float s0 = y & 1 ? high16(sv[i][0][y / 2]) : low16(sv[i][0][y / 2]);
+              const float s1 = y & 1 ? high16(sv[i][1][y / 2]) : low16(sv[i][1][y / 2]);
+              const uint32_t w0 = transpose8(pack_f16(p[0] * s0, p[1] * s0));
+              const uint32_t w1 = transpose8(pack_f16(p[2] * s1, p[3] * s1));
+              const uint32_t one = g == y ? 0x3c003c00u : 0u;
+              mma_f16(asum, one, 0u, one, 0u, w0, w1);
+              if constexpr (FMT == STEM_KV_Q4) {
+                const uint32_t va = vw[0][y], vb = vw[1][y];
+                mma_f16(acc[2 * y], va & 0x000f000fu, va & 0x00f000f0u, vb & 0x000f000fu,
+                        vb & 0x00f000f0u, w0, w1);
+                mma_f16(acc[2 * y + 1], va >> 8 & 0x000f000fu, va >> 8 & 0x00f000f0u,
+                        vb >> 8 & 0x000f000fu, vb >> 8 & 0x00f000f0u, w0, w1);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint32_t va = vw[0][2 * y + x], vb = vw[1][2 * y + x];
+                  mma_f16(acc[2 * y + x], va & 0x00ff00ffu, va >> 8 & 0x00ff00ffu,
+                          vb & 0x00ff00ffu, vb >> 8 & 0x00ff00ffu, w0, w1);
+                }
               }
             }
           }
         }
       }
       __syncwarp();
-      fetch(u + (C::STAGES - 1) * kWarps, (stage + C::STAGES - 1) % C::STAGES);
       stage = stage + 1 == C::STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
@@ -504,21 +608,25 @@ __global__ void __launch_bounds__(kWarps * 32) attn_kernel(const Args a) {
           acc[n][3] = (acc[n][3] * second - off1) * inv;
         }
       }
+      x0 = l0;
+      x1 = l1;
     }
 #pragma unroll
     for (int o = 4; o < 32; o *= 2) {
       l0 += __shfl_xor_sync(kFull, l0, o);
       l1 += __shfl_xor_sync(kFull, l1, o);
+      x0 += __shfl_xor_sync(kFull, x0, o);
+      x1 += __shfl_xor_sync(kFull, x1, o);
     }
   };
 
-  float* o_s = reinterpret_cast<float*>(smem);  // [kWarps][8][D], over the rings
   // Joins the warps' results for the heads in `heads` and writes them.
   auto finish = [&](uint32_t heads) {
     __syncthreads();
     if (g == 0) {
       s_m[warp][2 * t] = m0, s_m[warp][2 * t + 1] = m1;
       s_l[warp][2 * t] = l0, s_l[warp][2 * t + 1] = l1;
+      s_x[warp][2 * t] = x0, s_x[warp][2 * t + 1] = x1;
     }
     float* o = o_s + warp * kHeadTile * D;
 #pragma unroll
@@ -537,39 +645,37 @@ __global__ void __launch_bounds__(kWarps * 32) attn_kernel(const Args a) {
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_m[w][h]);
       const float base = m == -INFINITY ? 0.f : m;
-      float x = 0.f, l = 0.f;
+      float x = 0.f, l = 0.f, lx = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         if (s_m[w][h] == -INFINITY && s_l[w][h] == 0.f) continue;  // saw nothing of this head
         const float f = exp2f(s_m[w][h] - base);
         x = fmaf(f, o_s[(w * kHeadTile + h) * D + d], x);
         l = fmaf(f, s_l[w][h], l);
+        lx = fmaf(f, s_x[w][h], lx);
       }
       if (a.splits == 1) {
         a.out[(head0 + h) * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-        if (d == 0 && a.lse) a.lse[head0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (d == 0 && a.lse) a.lse[head0 + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
       } else {
-        float* q = a.part + (((static_cast<int64_t>(row) * gridDim.y + blockIdx.y) * a.splits +
-                              blockIdx.x) * kHeadTile + h) * (D + 2);
-        q[d] = x;
-        if (d == 0) q[D] = m, q[D + 1] = l;
+        a.part[(item * kHeadTile + h) * D + d] = x;
+        if (d == 0) a.stat[item * kHeadTile + h] = make_float4(m, l, lx, 0.f);
       }
     }
   };
 
   stream(0xffu);
-  // With 16-bit values a head that does not keep a block still meets its V rows with weight 0, and
-  // 0 * NaN or 0 * inf is not 0. That shows as a NaN: such a CTA goes over its entries once more for
-  // each head alone, so that a head meets only blocks it keeps.
-  if constexpr (!kQuant) {
-    if (!a.share && nh > 1) {
-      bool nan = false;
+  // A head that does not keep a block still meets its V rows with weight 0, and 0 * NaN or 0 * inf
+  // (of a 16-bit value or of a scale) is not 0. That shows as a NaN: such a CTA goes over its entries
+  // once more for each head alone, so that a head meets only blocks it keeps.
+  bool odd = false;
+  if (!a.share && nh > 1) {
+    bool nan = false;
 #pragma unroll
-      for (int n = 0; n < 2 * NG; ++n)
+    for (int n = 0; n < 2 * NG; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) nan |= isnan(acc[n][e]);
-      odd = __syncthreads_or(nan);
-    }
+      for (int e = 0; e < 4; ++e) nan |= isnan(acc[n][e]);
+    odd = __syncthreads_or(nan);
   }
   if (!odd) {
     finish(0xffu);
@@ -582,77 +688,142 @@ __global__ void __launch_bounds__(kWarps * 32) attn_kernel(const Args a) {
   }
 }
 
-// Joins the CTAs of each item: one CTA per (row, query head), a thread per channel.
+// Joins the parts of each item: one CTA per (row, query head). Threads first turn the parts'
+// maxima into weights, then groups of D threads sum the numerators of every kGroups-th part.
+constexpr int kJoinThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(D) join_kernel(const Args a) {
-  const int row = blockIdx.y, head = blockIdx.x, d = threadIdx.x;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
+  constexpr int kGroups = kJoinThreads / D, kJoinWarps = kJoinThreads / 32;
+  extern __shared__ float weight[];  // splits
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps], s_o[kGroups][D];
+  const int row = blockIdx.y, head = blockIdx.x, tid = threadIdx.x;
   const int G = a.r.Hq / a.c.Hkv, tiles_h = (G + kHeadTile - 1) / kHeadTile;
-  const int item = head / G * tiles_h + head % G / kHeadTile, h = head % G % kHeadTile;
-  const float* p = a.part + ((static_cast<int64_t>(row) * a.c.Hkv * tiles_h + item) * a.splits *
-                                 kHeadTile + h) * (D + 2);
-  const int64_t step = static_cast<int64_t>(kHeadTile) * (D + 2);
+  const int h = head % G % kHeadTile;
+  const int64_t item = static_cast<int64_t>(row) * a.c.Hkv * tiles_h + head / G * tiles_h +
+                       head % G / kHeadTile;
+  const float4* stat = a.stat + item * a.splits * kHeadTile + h;
+  const float* part = a.part + (item * a.splits * kHeadTile + h) * D;
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
   float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, p[s * step + D]);
+  for (int s = tid; s < a.splits; s += kJoinThreads) m = fmaxf(m, stat[s * kHeadTile].x);
+  for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  if (tid % 32 == 0) s_m[tid / 32] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
   const float base = m == -INFINITY ? 0.f : m;
-  float x = 0.f, l = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float ms = p[s * step + D], ls = p[s * step + D + 1];
-    if (ms == -INFINITY && ls == 0.f) continue;
-    const float f = exp2f(ms - base);
-    x = fmaf(f, p[s * step + d], x);
-    l = fmaf(f, ls, l);
+  float l = 0.f, lx = 0.f;
+  for (int s = tid; s < a.splits; s += kJoinThreads) {
+    const float4 st = stat[s * kHeadTile];
+    const bool none = st.x == -INFINITY && st.y == 0.f;  // (its numerators were not written)
+    const float f = exp2f(st.x - base);
+    weight[s] = none ? -1.f : f;
+    if (!none) {
+      l = fmaf(f, st.y, l);
+      lx = fmaf(f, st.z, lx);
+    }
   }
-  const int64_t o = static_cast<int64_t>(row) * a.r.Hq + head;
-  a.out[o * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-  if (d == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int o = 16; o; o /= 2) {
+    l += __shfl_xor_sync(kFull, l, o);
+    lx += __shfl_xor_sync(kFull, lx, o);
+  }
+  if (tid % 32 == 0) s_l[tid / 32] = l, s_x[tid / 32] = lx;
+  __syncthreads();
+  const int d = tid % D, grp = tid / D;
+  float x = 0.f;
+#pragma unroll 4
+  for (int s = grp; s < a.splits; s += kGroups) {
+    const float f = weight[s];
+    if (f >= 0.f || isnan(f)) x = fmaf(f, part[static_cast<int64_t>(s) * kHeadTile * D + d], x);
+  }
+  s_o[grp][d] = x;
+  __syncthreads();
+  if (grp == 0) {
+    l = s_l[0], lx = s_x[0];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) l += s_l[w], lx += s_x[w];
+#pragma unroll
+    for (int n = 1; n < kGroups; ++n) x += s_o[n][d];
+    const int64_t o = static_cast<int64_t>(row) * a.r.Hq + head;
+    a.out[o * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
+    if (d == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+  }
 }
 
-// Split of the longest item's list over CTAs.
+// Split of an item's list over CTAs: enough of them to fill the device when there are few items, and
+// no longer than kChunkBytes of K and V, so that rows of unequal length even out.
+constexpr int kChunkBytes = 256 << 10;
+
 struct Split {
   int chunk, splits;
 };
-Split split_of(int Hkv, int max_blocks, int R, int Hq, int kcap, bool share) {
+Split split_of(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq, int kcap,
+               bool share) {
   const int G = Hq / Hkv;
   const int64_t items = static_cast<int64_t>(R) * Hkv * ((G + kHeadTile - 1) / kHeadTile);
   // entries of an item's list: one list, or the union of its heads' lists
   const int64_t most =
       share ? kcap : std::min<int64_t>(static_cast<int64_t>(std::min(G, kHeadTile)) * kcap,
                                        max_blocks);
-  const int64_t target = 8 * static_cast<int64_t>(sm_count());
-  int64_t chunk = std::max<int64_t>(1, most * items / target);
+  const int64_t fill = most * items / (3 * static_cast<int64_t>(sm_count()));
+  const int64_t even = kChunkBytes / kv_record_bytes(kv_tile_bytes(format, D), block);
   Split s;
+  const int64_t chunk = std::max<int64_t>(1, std::min(fill, even));
   s.chunk = static_cast<int>(chunk);
   s.splits = static_cast<int>((most + chunk - 1) / chunk);
   return s;
+}
+int64_t parts_of(int Hkv, int R, int Hq, int splits) {
+  const int G = Hq / Hkv;
+  return static_cast<int64_t>(R) * Hkv * ((G + kHeadTile - 1) / kHeadTile) * splits * kHeadTile;
+}
+
+// Launches on a stream whose previous kernel may still be running: the kernels wait for it
+// themselves (cudaGridDependencySynchronize), after they have been set up.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int FMT, int D>
 cudaError_t launch(const Args& a, cudaStream_t st) {
   using C = Cfg<FMT, D>;
   const int G = a.r.Hq / a.c.Hkv;
-  const size_t ring = static_cast<size_t>(kWarps) * C::RING;
   static_assert(C::RING >= kHeadTile * D * 4, "the rings hold the warps' results at the end");
-  const size_t bytes = ring + 4 * static_cast<size_t>(a.chunk) + 4 * ((a.c.max_blocks + 3) / 4);
+  const size_t bytes = static_cast<size_t>(kWarps) * C::RING + sizeof(Entry) * a.chunk +
+                       (a.share ? 0 : 4 * ((a.c.max_blocks + 3) / 4));
   // the attribute is per device; setting it is cheap and idempotent
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<FMT, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
   const dim3 grid(a.splits, a.c.Hkv * ((G + kHeadTile - 1) / kHeadTile), a.r.R);
-  attn_kernel<FMT, D><<<grid, kWarps * 32, bytes, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_after(attn_kernel<FMT, D>, grid, kWarps * 32, bytes, st, a);
   if (e != cudaSuccess || a.splits == 1) return e;
-  join_kernel<D><<<dim3(a.r.Hq, a.r.R), D, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(join_kernel<D>, dim3(a.r.Hq, a.r.R), kJoinThreads, 4 * a.splits, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
                                void* out, float* lse, float* partials, cudaStream_t st) {
-  const Split s = split_of(c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
+  const Split s = split_of(format, D, c.block, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
+  const int64_t parts = parts_of(c.Hkv, r.R, r.Hq, s.splits);
   const Args a{c,   r, share, s.chunk, s.splits, static_cast<__nv_bfloat16*>(out), lse,
-               partials};
+               reinterpret_cast<float4*>(partials), partials + 4 * parts};
   if (D == 128) {
     switch (format) {
       case STEM_KV_BF16: return launch<STEM_KV_BF16, 128>(a, st);
@@ -667,13 +838,10 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   }
 }
 
-size_t decode_attn_partials(int, int D, int Hkv, int max_blocks, int R, int Hq, int kcap,
-                            bool share) {
-  const Split s = split_of(Hkv, max_blocks, R, Hq, kcap, share);
-  if (s.splits == 1) return 0;
-  const int G = Hq / Hkv;
-  return static_cast<size_t>(R) * Hkv * ((G + kHeadTile - 1) / kHeadTile) * s.splits * kHeadTile *
-         (D + 2);
+size_t decode_attn_partials(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq,
+                            int kcap, bool share) {
+  const Split s = split_of(format, D, block, Hkv, max_blocks, R, Hq, kcap, share);
+  return s.splits == 1 ? 0 : static_cast<size_t>(parts_of(Hkv, R, Hq, s.splits)) * (4 + D);
 }
 
 }  // namespace stem

@@ -39,7 +39,7 @@ cudaError_t launch_decode_select(const KvCache& c, int D, const DecodeRows& r,
 // list (that of the first). partials: decode_attn_partials() floats.
 cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
                                void* out, float* lse, float* partials, cudaStream_t st);
-size_t decode_attn_partials(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap,
-                            bool share);
+size_t decode_attn_partials(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq,
+                            int kcap, bool share);
 
 }  // namespace stem
