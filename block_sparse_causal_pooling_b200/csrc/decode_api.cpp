@@ -94,25 +94,24 @@ int cache_rows(bool write, const stem_cache_t* c, void* k, void* v, int dtype, i
 // ------------------------------------------------------------------ decode
 
 struct Layout {
-  size_t scores = 0, partials = 0, total = 0;
+  size_t scores = 0, attn = 0, total = 0;
 };
 
-// The partials' size depends on whether heads share lists: the larger of the two is reserved, so
+// The attention's part depends on whether heads share lists: the larger of the two is reserved, so
 // that one size serves every method.
 Layout layout(const stem_cache_t* c, int R, int Hq, int kcap) {
   Layout L;
   size_t o = 0;
   L.scores = o;
   o += align_up(sizeof(double) * static_cast<size_t>(R) * Hq * c->max_blocks);
-  L.partials = o;
-  size_t part = 0;
+  L.attn = o;
+  size_t most = 0;
   for (int share = 0; share < 2; ++share) {
-    const size_t n = decode_attn_partials(c->format, c->D, c->block, c->Hkv, c->max_blocks, R, Hq,
-                                          kcap, share != 0);
-    if (n > part) part = n;
+    const size_t n = decode_attn_bytes(c->format, c->D, c->Hkv, c->max_blocks, R, Hq, kcap,
+                                       share != 0);
+    if (n > most) most = n;
   }
-  o += align_up(sizeof(float) * part);
-  L.total = o;
+  L.total = o + align_up(most);
   return L;
 }
 
@@ -120,7 +119,9 @@ int check_shape(const stem_cache_t* c, int R, int Hq, int kcap) {
   const int rc = check_cache(c);
   if (rc != STEM_OK) return rc;
   if (R < 0 || Hq < 1 || Hq % c->Hkv != 0 || kcap < 1 || kcap > c->max_blocks) return STEM_ERR_ARG;
-  if (R > kMaxGrid || Hq > kMaxGrid) return STEM_ERR_UNSUPPORTED;
+  if (R > kMaxGrid || Hq > kMaxGrid ||
+      static_cast<int64_t>(R) * Hq * c->max_blocks > 0x7fffffffLL)
+    return STEM_ERR_UNSUPPORTED;
   return STEM_OK;
 }
 
@@ -180,7 +181,7 @@ int run_decode(const stem_decode_args_t* a, bool select, bool attend, cudaStream
   }
   if (!attend) return STEM_OK;
   return cuda_err(launch_decode_attn(c, a->cache->format, a->cache->D, r, share, a->out, a->lse,
-                                     reinterpret_cast<float*>(ws + L.partials), st));
+                                     ws + L.attn, st));
 }
 
 }  // namespace

@@ -41,6 +41,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4;
 constexpr int kHeadTile = 8;
+constexpr int kStaged = 128;  // list entries in shared memory at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A logit may exceed the running maximum by this much (in log2 units) before the accumulators are
@@ -121,73 +122,98 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float low16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-struct Args {
-  KvCache c;
-  DecodeRows r;
-  bool share;
-  int chunk;   // list entries of a CTA
-  int splits;  // CTAs of an item
-  __nv_bfloat16* out;
-  float* lse;
-  // [R][Hkv * head tiles][splits][8] of each part of an item: statistics (max in log2 units, sum
-  // for the output, sum for lse) and [D] numerators
-  float4* stat;
-  float* part;
-};
-
-// An entry of an item's list: the block's page, the block | query heads that keep it << 16.
+// An entry of a list: the block's page, the block | query heads that keep it << 16.
 struct Entry {
   int page;
   uint32_t what;
 };
-__device__ __forceinline__ Entry entry_of(const Args& a, int seq, int j, uint32_t heads) {
-  const int page = kv_page(a.c, seq, j, a.r.status);
+__device__ __forceinline__ Entry entry_of(const KvCache& c, int seq, int j, uint32_t heads,
+                                          int32_t* status) {
+  const int page = kv_page(c, seq, j, status);
   return page < 0 ? Entry{0, 0u} : Entry{page, static_cast<uint32_t>(j) | heads << 16};
 }
 
-// The entries of this CTA's part of its item's list; an invalid one has no heads.
-__device__ __forceinline__ int build_list(const Args& a, int row, int seq, int kv, int h0, int nh,
-                                          int last, Entry* ent, uint32_t* mask, uint32_t* wbuf) {
-  const int tid = threadIdx.x, G = a.r.Hq / a.c.Hkv;
-  const int e0 = blockIdx.x * a.chunk;
-  const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G;
-  const uint32_t none = 0xffu << nh & 0xffu;  // columns without a head go along with any block
+struct Args {
+  KvCache c;
+  DecodeRows r;
+  bool share;
+  int tiles_h;  // head tiles of a kv head
+  int items;    // R * Hkv * tiles_h: a row, a kv head and up to 8 of its query heads
+  int most;     // entries a list may have
+  // One list of blocks for each (row, kv head) where its heads share it, else for each item.
+  Entry* list;     // [lists][most]
+  int32_t* count;  // [lists]
+  // Entry numbers run over the items in order; CTA n of N = min(ctas, total) takes total * n / N and
+  // up (at least one).
+  int ctas;
+  int64_t* start;  // [items]: number of the item's first entry; [items]: total
+  __nv_bfloat16* out;
+  float* lse;
+  // [2 * ctas][8] statistics (max in log2 units, sum for the output, sum for lse) and [D] numerators
+  // of the items that a CTA has a part of: its first one, and its last one
+  float4* stat;
+  float* part;
+};
+
+// ------------------------------------------------------------------ the lists
+
+constexpr int kPlanThreads = 128;
+
+// Turns the kept blocks of each (row, kv head) or item into a list of entries: the page of each
+// block and the heads that keep it. One CTA per list.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
+  extern __shared__ uint32_t mask[];  // per-head lists: a byte of head bits for each block
+  __shared__ uint32_t wbuf[kPlanThreads / 32];
+  const int tid = threadIdx.x, row = blockIdx.y, G = a.r.Hq / a.c.Hkv;
+  const int64_t list = static_cast<int64_t>(row) * gridDim.x + blockIdx.x;
+  Entry* out = a.list + list * a.most;
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+  int seq, len;
+  decode_row(a.c, a.r, row, seq, len);
+  const int last = (len + a.c.block - 1) / a.c.block - 1;
+  if (last < 0) {
+    if (tid == 0) a.count[list] = 0;
+    return;
+  }
   if (a.share) {
-    const int cnt = a.r.sel_cnt[head0];
+    const int64_t head = static_cast<int64_t>(row) * a.r.Hq + blockIdx.x * G;
+    const int cnt = a.r.sel_cnt[head];
     if ((cnt < 0 || cnt > a.r.kcap) && a.r.status) *a.r.status = STEM_ERR_ARG;
-    const int n = min(max(min(cnt, a.r.kcap) - e0, 0), a.chunk);
-    const int32_t* idx = a.r.sel_idx + head0 * a.r.kcap + e0;
-    for (int e = tid; e < n; e += kWarps * 32) {
-      const int j = idx[e];
+    const int n = max(min(cnt, a.r.kcap), 0);
+    for (int e = tid; e < n; e += kPlanThreads) {
+      const int j = a.r.sel_idx[head * a.r.kcap + e];
       if (j >= 0 && j <= last) {
-        ent[e] = entry_of(a, seq, j, 0xffu);
+        out[e] = entry_of(a.c, seq, j, 0xffu, a.r.status);
       } else {
         if (a.r.status) *a.r.status = STEM_ERR_ARG;
-        ent[e] = Entry{0, 0u};
+        out[e] = Entry{0, 0u};
       }
     }
-    __syncthreads();
-    return n;
+    if (tid == 0) a.count[list] = n;
+    return;
   }
-  // union of the heads' lists: a byte of head bits for each block
+  // the union of the heads' lists, in block order
+  const int kv = blockIdx.x / a.tiles_h, h0 = blockIdx.x % a.tiles_h * kHeadTile;
+  const int nh = min(G - h0, kHeadTile);
+  const uint32_t none = 0xffu << nh & 0xffu;  // columns without a head go along with any block
+  const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
   const int words = (last + 4) / 4;
-  for (int w = tid; w < words; w += kWarps * 32) mask[w] = 0;
+  for (int w = tid; w < words; w += kPlanThreads) mask[w] = 0;
   __syncthreads();
-  for (int h = 0; h < nh; ++h) {
-    const int64_t hd = head0 + h0 + h;
-    const int cnt = a.r.sel_cnt[hd];
-    if ((cnt < 0 || cnt > a.r.kcap) && a.r.status) *a.r.status = STEM_ERR_ARG;
-    for (int e = tid; e < min(cnt, a.r.kcap); e += kWarps * 32) {
-      const int j = a.r.sel_idx[hd * a.r.kcap + e];
-      if (j >= 0 && j <= last)
-        atomicOr(&mask[j / 4], 1u << (8 * (j % 4) + h));
-      else if (a.r.status)
-        *a.r.status = STEM_ERR_ARG;
-    }
+  for (int n = tid; n < nh * a.r.kcap; n += kPlanThreads) {
+    const int h = n / a.r.kcap, e = n % a.r.kcap;
+    const int j = a.r.sel_idx[(head0 + h) * a.r.kcap + e];
+    const int cnt = a.r.sel_cnt[head0 + h];
+    if (e == 0 && (cnt < 0 || cnt > a.r.kcap) && a.r.status) *a.r.status = STEM_ERR_ARG;
+    if (e >= cnt) continue;
+    if (j >= 0 && j <= last)
+      atomicOr(&mask[j / 4], 1u << (8 * (j % 4) + h));
+    else if (a.r.status)
+      *a.r.status = STEM_ERR_ARG;
   }
   __syncthreads();
-  // thread t owns a run of words; entries in block order
-  const int run = (words + kWarps * 32 - 1) / (kWarps * 32);
+  const int run = (words + kPlanThreads - 1) / kPlanThreads;  // thread t owns a run of words
   const int w0 = min(tid * run, words), w1 = min(w0 + run, words);
   uint32_t n = 0;
   for (int w = w0; w < w1; ++w)
@@ -200,20 +226,63 @@ __device__ __forceinline__ int build_list(const Args& a, int row, int seq, int k
   if (tid % 32 == 31) wbuf[tid / 32] = s;
   __syncthreads();
   uint32_t total = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
     if (w < tid / 32) s += wbuf[w];
     total += wbuf[w];
   }
-  int at = static_cast<int>(s - n) - e0;
+  uint32_t at = s - n;
   for (int w = w0; w < w1; ++w)
     for (int b = 0; b < 4; ++b) {
       const uint32_t m = mask[w] >> (8 * b) & 0xffu;
-      if (!m) continue;
-      if (at >= 0 && at < a.chunk) ent[at] = entry_of(a, seq, 4 * w + b, m | none);
-      ++at;
+      if (m) out[at++] = entry_of(a.c, seq, 4 * w + b, m | none, a.r.status);
     }
+  if (tid == 0) a.count[list] = static_cast<int32_t>(total);
+}
+
+// ------------------------------------------------------------------ attention
+
+__device__ __forceinline__ int list_of(const Args& a, int item) {
+  return a.share ? item / a.tiles_h : item;
+}
+
+// Where a CTA starts: the total number of entries, and the item and the entry in it that its first
+// entry is. The CTA sums the counts of all items (every CTA the same ones, from L2).
+struct Begin {
+  int64_t total;
+  int item, entry;
+  int64_t start;  // number of the item's first entry
+};
+__device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int64_t* wsum) {
+  const int tid = threadIdx.x, run = (a.items + kWarps * 32 - 1) / (kWarps * 32);
+  const int i0 = min(tid * run, a.items), i1 = min(i0 + run, a.items);
+  int64_t n = 0;
+  for (int i = i0; i < i1; ++i) n += a.count[list_of(a, i)];
+  int64_t s = n;
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t y = __shfl_up_sync(kFull, s, o);
+    if (tid % 32 >= o) s += y;
+  }
+  if (tid % 32 == 31) wsum[tid / 32] = s;
   __syncthreads();
-  return min(max(static_cast<int>(total) - e0, 0), a.chunk);
+  int64_t total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < tid / 32) s += wsum[w];
+    total += wsum[w];
+  }
+  s -= n;
+  const int64_t first = total * blockIdx.x / max(min(static_cast<int64_t>(a.ctas), total), int64_t{1});
+  if (blockIdx.x < total && first >= s && first < s + n) {
+    int i = i0;
+    for (;; ++i) {
+      const int c = a.count[list_of(a, i)];
+      if (first < s + c) break;
+      s += c;
+    }
+    *sh = Begin{total, i, static_cast<int>(first - s), s};
+  } else if (blockIdx.x >= total && tid == 0) {
+    *sh = Begin{total, 0, 0, 0};  // more CTAs than entries
+  }
+  __syncthreads();
 }
 
 template <int FMT, int D>
@@ -223,21 +292,40 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
   constexpr bool kQuant = C::Q;
   constexpr int NG = L::NG, TPS = C::TPS;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint32_t wbuf[kWarps];
+  __shared__ Begin s_begin;
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ Entry ent[kStaged];
   __shared__ float s_m[kWarps][kHeadTile], s_l[kWarps][kHeadTile], s_x[kWarps][kHeadTile];
-  Entry* ent = reinterpret_cast<Entry*>(smem + kWarps * C::RING);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(ent + a.chunk);
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-  const int G = a.r.Hq / a.c.Hkv, tiles_h = (G + kHeadTile - 1) / kHeadTile;
-  const int row = blockIdx.z, kv = blockIdx.y / tiles_h, h0 = blockIdx.y % tiles_h * kHeadTile;
-  const int nh = min(G - h0, kHeadTile);
-  const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
+  const int G = a.r.Hq / a.c.Hkv;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
+  find_begin(a, &s_begin, s_sum);
+  const int64_t total = s_begin.total;
+  if (blockIdx.x == 0 && tid == 0) a.start[a.items] = total;
+  const int64_t ctas = min(static_cast<int64_t>(a.ctas), total);
+  if (blockIdx.x >= ctas) return;
+  const int64_t e_first = total * blockIdx.x / ctas, e_end = total * (blockIdx.x + 1) / ctas;
+  int item = s_begin.item, entry = s_begin.entry;
+  int64_t e_at = e_first;
+
+  // this CTA's part of one item after the other
+  for (; e_at < e_end; ++item, entry = 0) {
+  const int n_item = a.count[list_of(a, item)];
+  const int n_ent = static_cast<int>(min(static_cast<int64_t>(n_item - entry), e_end - e_at));
+  if (n_ent <= 0) continue;
+  const bool whole = n_ent == n_item;
+  const int slot = 2 * blockIdx.x + (e_at == e_first ? 0 : 1);
+  if (entry == 0 && tid == 0) a.start[item] = e_at;
+  e_at += n_ent;
+  const Entry* list = a.list + static_cast<int64_t>(list_of(a, item)) * a.most + entry;
+  const int row = item / (a.c.Hkv * a.tiles_h), kv = item / a.tiles_h % a.c.Hkv;
+  const int h0 = item % a.tiles_h * kHeadTile;
+  const int nh = min(G - h0, kHeadTile);
+  const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
   int seq, len;
   decode_row(a.c, a.r, row, seq, len);
-  const int last = (len + a.c.block - 1) / a.c.block - 1;
 
   // ---- the queries, as B operands: head g, channels 8t .. 8t + 7 of each group
   uint32_t qf[NG][4];
@@ -250,20 +338,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
       qf[y][0] = u.x, qf[y][1] = u.y, qf[y][2] = u.z, qf[y][3] = u.w;
     }
   }
-  const int n_ent = last >= 0 ? build_list(a, row, seq, kv, h0, nh, last, ent, mask, wbuf) : 0;
-
   float* o_s = reinterpret_cast<float*>(smem);  // [kWarps][8][D], over the rings at the end
-  const int64_t item = (static_cast<int64_t>(row) * gridDim.y + blockIdx.y) * a.splits + blockIdx.x;
-  if (n_ent == 0) {  // nothing here
-    if (a.splits > 1) {
-      if (tid < kHeadTile) a.stat[item * kHeadTile + tid] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    } else {
-      for (int n = tid; n < nh * D; n += kWarps * 32) a.out[head0 * D + n] = __float2bfloat16_rn(0.f);
-      if (tid < nh && a.lse) a.lse[head0 + tid] = -INFINITY;
-    }
-    return;
-  }
-
   float qscale = kLog2e / sqrtf(static_cast<float>(D));  // of head g: logits in log2 units
   float cinit[NG][2];
   if constexpr (kQuant) {
@@ -313,11 +388,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
   int vlim;              // largest scale (bf16 bits) that vf is good for
   unsigned char* ring = smem + warp * C::RING;
   const int spb_log = a.c.block / C::STEP == 2 ? 1 : a.c.block / C::STEP == 4 ? 2 : 3;
-  const int units = n_ent << spb_log;
   const int64_t page_bytes = static_cast<int64_t>(a.c.Hkv) * a.c.record;
   const unsigned char* head_pages = a.c.at(0, kv) + lane * 16;
 
-  // Streams the steps of the entries that one of `heads` keeps.
+  // Goes over the steps of the entries that one of `heads` keeps.
   auto stream = [&](uint32_t heads) {
 #pragma unroll
     for (int n = 0; n < 2 * NG; ++n)
@@ -329,6 +403,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
     l0 = l1 = x0 = x1 = 0.f;
     vf = 1.f;
     vlim = -1;
+    for (int e0 = 0; e0 < n_ent; e0 += kStaged) {
+    __syncthreads();
+    const int n_now = min(n_ent - e0, kStaged);
+    for (int n = tid; n < n_now; n += kWarps * 32) ent[n] = list[e0 + n];
+    __syncthreads();
+    const int units = n_now << spb_log;
 
     // tokens of step u that are there, 0 or less where there is nothing to do
     auto tokens = [&](int u, const Entry& e) -> int {
@@ -590,6 +670,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
     }
     cp_wait<0>();
     __syncwarp();
+    }
 
     // ---- numerators in units of V: o = sum_t p_t V_t relative to 2^m
     if constexpr (kQuant) {
@@ -654,12 +735,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
         l = fmaf(f, s_l[w][h], l);
         lx = fmaf(f, s_x[w][h], lx);
       }
-      if (a.splits == 1) {
+      if (whole) {
         a.out[(head0 + h) * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
         if (d == 0 && a.lse) a.lse[head0 + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
       } else {
-        a.part[(item * kHeadTile + h) * D + d] = x;
-        if (d == 0) a.stat[item * kHeadTile + h] = make_float4(m, l, lx, 0.f);
+        a.part[(static_cast<int64_t>(slot) * kHeadTile + h) * D + d] = x;
+        if (d == 0) a.stat[slot * kHeadTile + h] = make_float4(m, l, lx, 0.f);
       }
     }
   };
@@ -683,31 +764,44 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
     for (int h = 0; h < nh; ++h) {
       stream(1u << h);
       finish(1u << h);
-      __syncthreads();
     }
+  }
+  __syncthreads();  // (the results in shared memory have been read)
   }
 }
 
-// Joins the parts of each item: one CTA per (row, query head). Threads first turn the parts'
-// maxima into weights, then groups of D threads sum the numerators of every kGroups-th part.
+// Joins the items that several CTAs have a part of (and writes those without a block): one CTA per
+// (row, query head). Threads first turn the parts' maxima into weights, then groups of D threads sum
+// the numerators of every kGroups-th part.
 constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   constexpr int kGroups = kJoinThreads / D, kJoinWarps = kJoinThreads / 32;
-  extern __shared__ float weight[];  // splits
+  extern __shared__ float weight[];  // ctas
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps], s_o[kGroups][D];
   const int row = blockIdx.y, head = blockIdx.x, tid = threadIdx.x;
-  const int G = a.r.Hq / a.c.Hkv, tiles_h = (G + kHeadTile - 1) / kHeadTile;
-  const int h = head % G % kHeadTile;
-  const int64_t item = static_cast<int64_t>(row) * a.c.Hkv * tiles_h + head / G * tiles_h +
-                       head % G / kHeadTile;
-  const float4* stat = a.stat + item * a.splits * kHeadTile + h;
-  const float* part = a.part + (item * a.splits * kHeadTile + h) * D;
+  const int G = a.r.Hq / a.c.Hkv, h = head % G % kHeadTile;
+  const int item = (row * a.c.Hkv + head / G) * a.tiles_h + head % G / kHeadTile;
+  const int64_t o_at = static_cast<int64_t>(row) * a.r.Hq + head;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
+  const int n = a.count[list_of(a, item)];
+  if (n == 0) {
+    if (tid < D) a.out[o_at * D + tid] = __float2bfloat16_rn(0.f);
+    if (tid == 0 && a.lse) a.lse[o_at] = -INFINITY;
+    return;
+  }
+  // CTA n takes entries total * n / N and up, so entry e is with CTA ((e + 1) N - 1) / total
+  const int64_t total = a.start[a.items], e0 = a.start[item];
+  const int64_t ctas = min(static_cast<int64_t>(a.ctas), total);
+  const int c0 = static_cast<int>(((e0 + 1) * ctas - 1) / total);
+  const int parts = static_cast<int>(((e0 + n) * ctas - 1) / total) - c0 + 1;
+  if (parts == 1) return;  // (its CTA has written the output)
+  const int first = total * c0 / ctas == e0 ? 0 : 1;  // the item is its first CTA's first or last
+  auto slot = [&](int s) { return 2 * (c0 + s) + (s == 0 ? first : 0); };
   float m = -INFINITY;
-  for (int s = tid; s < a.splits; s += kJoinThreads) m = fmaxf(m, stat[s * kHeadTile].x);
+  for (int s = tid; s < parts; s += kJoinThreads) m = fmaxf(m, a.stat[slot(s) * kHeadTile + h].x);
   for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
   if (tid % 32 == 0) s_m[tid / 32] = m;
   __syncthreads();
@@ -715,15 +809,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f, lx = 0.f;
-  for (int s = tid; s < a.splits; s += kJoinThreads) {
-    const float4 st = stat[s * kHeadTile];
-    const bool none = st.x == -INFINITY && st.y == 0.f;  // (its numerators were not written)
+  for (int s = tid; s < parts; s += kJoinThreads) {
+    const float4 st = a.stat[slot(s) * kHeadTile + h];
     const float f = exp2f(st.x - base);
-    weight[s] = none ? -1.f : f;
-    if (!none) {
-      l = fmaf(f, st.y, l);
-      lx = fmaf(f, st.z, lx);
-    }
+    weight[s] = f;
+    l = fmaf(f, st.y, l);
+    lx = fmaf(f, st.z, lx);
   }
   for (int o = 16; o; o /= 2) {
     l += __shfl_xor_sync(kFull, l, o);
@@ -732,12 +823,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   if (tid % 32 == 0) s_l[tid / 32] = l, s_x[tid / 32] = lx;
   __syncthreads();
   const int d = tid % D, grp = tid / D;
+  const float* part = a.part + static_cast<int64_t>(h) * D + d;
   float x = 0.f;
-#pragma unroll 4
-  for (int s = grp; s < a.splits; s += kGroups) {
-    const float f = weight[s];
-    if (f >= 0.f || isnan(f)) x = fmaf(f, part[static_cast<int64_t>(s) * kHeadTile * D + d], x);
-  }
+#pragma unroll 8
+  for (int s = grp; s < parts; s += kGroups)
+    x = fmaf(weight[s], part[static_cast<int64_t>(slot(s)) * kHeadTile * D], x);
   s_o[grp][d] = x;
   __syncthreads();
   if (grp == 0) {
@@ -745,39 +835,47 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
 #pragma unroll
     for (int w = 1; w < kJoinWarps; ++w) l += s_l[w], lx += s_x[w];
 #pragma unroll
-    for (int n = 1; n < kGroups; ++n) x += s_o[n][d];
-    const int64_t o = static_cast<int64_t>(row) * a.r.Hq + head;
-    a.out[o * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-    if (d == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+    for (int i = 1; i < kGroups; ++i) x += s_o[i][d];
+    a.out[o_at * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
+    if (d == 0 && a.lse) a.lse[o_at] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
   }
 }
 
-// Split of an item's list over CTAs: enough of them to fill the device when there are few items, and
-// no longer than kChunkBytes of K and V, so that rows of unequal length even out.
-constexpr int kChunkBytes = 256 << 10;
-
-struct Split {
-  int chunk, splits;
+// Sizes of a call, and where its arrays are in the workspace.
+struct Sizes {
+  int tiles_h, most, ctas;
+  int64_t items, lists;
+  size_t list, count, start, stat, part, total;
 };
-Split split_of(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq, int kcap,
-               bool share) {
+Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap, bool share) {
+  Sizes s;
   const int G = Hq / Hkv;
-  const int64_t items = static_cast<int64_t>(R) * Hkv * ((G + kHeadTile - 1) / kHeadTile);
-  // entries of an item's list: one list, or the union of its heads' lists
-  const int64_t most =
-      share ? kcap : std::min<int64_t>(static_cast<int64_t>(std::min(G, kHeadTile)) * kcap,
-                                       max_blocks);
-  const int64_t fill = most * items / (3 * static_cast<int64_t>(sm_count()));
-  const int64_t even = kChunkBytes / kv_record_bytes(kv_tile_bytes(format, D), block);
-  Split s;
-  const int64_t chunk = std::max<int64_t>(1, std::min(fill, even));
-  s.chunk = static_cast<int>(chunk);
-  s.splits = static_cast<int>((most + chunk - 1) / chunk);
+  s.tiles_h = (G + kHeadTile - 1) / kHeadTile;
+  s.items = static_cast<int64_t>(R) * Hkv * s.tiles_h;
+  s.lists = share ? static_cast<int64_t>(R) * Hkv : s.items;
+  // one list, or the union of its heads' lists
+  s.most = share ? kcap
+                 : static_cast<int>(std::min<int64_t>(
+                       static_cast<int64_t>(std::min(G, kHeadTile)) * kcap, max_blocks));
+  // as many CTAs as run at once, so that each gets the same number of blocks
+  const int per_sm = format == STEM_KV_Q4 ? Cfg<STEM_KV_Q4, 128>::CTAS
+                     : format == STEM_KV_Q8 ? Cfg<STEM_KV_Q8, 128>::CTAS
+                                            : Cfg<STEM_KV_BF16, 128>::CTAS;
+  s.ctas = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(sm_count()) * per_sm,
+                                              s.items * s.most));
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  s.list = take(sizeof(Entry) * static_cast<size_t>(s.lists) * s.most);
+  s.count = take(sizeof(int32_t) * static_cast<size_t>(s.lists));
+  s.start = take(sizeof(int64_t) * static_cast<size_t>(s.items + 1));
+  s.stat = take(sizeof(float4) * 2 * static_cast<size_t>(s.ctas) * kHeadTile);
+  s.part = take(sizeof(float) * 2 * static_cast<size_t>(s.ctas) * kHeadTile * D);
+  s.total = o;
   return s;
-}
-int64_t parts_of(int Hkv, int R, int Hq, int splits) {
-  const int G = Hq / Hkv;
-  return static_cast<int64_t>(R) * Hkv * ((G + kHeadTile - 1) / kHeadTile) * splits * kHeadTile;
 }
 
 // Launches on a stream whose previous kernel may still be running: the kernels wait for it
@@ -801,29 +899,42 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 template <int FMT, int D>
 cudaError_t launch(const Args& a, cudaStream_t st) {
   using C = Cfg<FMT, D>;
-  const int G = a.r.Hq / a.c.Hkv;
   static_assert(C::RING >= kHeadTile * D * 4, "the rings hold the warps' results at the end");
-  const size_t bytes = static_cast<size_t>(kWarps) * C::RING + sizeof(Entry) * a.chunk +
-                       (a.share ? 0 : 4 * ((a.c.max_blocks + 3) / 4));
-  // the attribute is per device; setting it is cheap and idempotent
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<FMT, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(bytes));
+  const size_t mask = a.share ? 0 : 4 * ((a.c.max_blocks + 3) / 4);
+  cudaError_t e = launch_after(
+      plan_kernel, dim3(a.share ? a.c.Hkv : a.c.Hkv * a.tiles_h, a.r.R), kPlanThreads, mask, st, a);
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.splits, a.c.Hkv * ((G + kHeadTile - 1) / kHeadTile), a.r.R);
-  e = launch_after(attn_kernel<FMT, D>, grid, kWarps * 32, bytes, st, a);
-  if (e != cudaSuccess || a.splits == 1) return e;
-  return launch_after(join_kernel<D>, dim3(a.r.Hq, a.r.R), kJoinThreads, 4 * a.splits, st, a);
+  constexpr size_t bytes = static_cast<size_t>(kWarps) * C::RING;
+  // the attribute is per device; setting it is cheap and idempotent
+  e = cudaFuncSetAttribute(attn_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e != cudaSuccess) return e;
+  e = launch_after(attn_kernel<FMT, D>, dim3(a.ctas), kWarps * 32, bytes, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_after(join_kernel<D>, dim3(a.r.Hq, a.r.R), kJoinThreads, sizeof(float) * a.ctas,
+                      st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
-                               void* out, float* lse, float* partials, cudaStream_t st) {
-  const Split s = split_of(format, D, c.block, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
-  const int64_t parts = parts_of(c.Hkv, r.R, r.Hq, s.splits);
-  const Args a{c,   r, share, s.chunk, s.splits, static_cast<__nv_bfloat16*>(out), lse,
-               reinterpret_cast<float4*>(partials), partials + 4 * parts};
+                               void* out, float* lse, unsigned char* ws, cudaStream_t st) {
+  const Sizes s = sizes_of(format, D, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
+  Args a;
+  a.c = c;
+  a.r = r;
+  a.share = share;
+  a.tiles_h = s.tiles_h;
+  a.items = static_cast<int>(s.items);
+  a.most = s.most;
+  a.list = reinterpret_cast<Entry*>(ws + s.list);
+  a.count = reinterpret_cast<int32_t*>(ws + s.count);
+  a.ctas = s.ctas;
+  a.start = reinterpret_cast<int64_t*>(ws + s.start);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.stat = reinterpret_cast<float4*>(ws + s.stat);
+  a.part = reinterpret_cast<float*>(ws + s.part);
   if (D == 128) {
     switch (format) {
       case STEM_KV_BF16: return launch<STEM_KV_BF16, 128>(a, st);
@@ -838,10 +949,9 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   }
 }
 
-size_t decode_attn_partials(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq,
-                            int kcap, bool share) {
-  const Split s = split_of(format, D, block, Hkv, max_blocks, R, Hq, kcap, share);
-  return s.splits == 1 ? 0 : static_cast<size_t>(parts_of(Hkv, R, Hq, s.splits)) * (4 + D);
+size_t decode_attn_bytes(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap,
+                         bool share) {
+  return sizes_of(format, D, Hkv, max_blocks, R, Hq, kcap, share).total;
 }
 
 }  // namespace stem

@@ -36,10 +36,10 @@ cudaError_t launch_decode_select(const KvCache& c, int D, const DecodeRows& r,
                                  cudaStream_t st);
 
 // Attention over the kept blocks (decode_attn.cu). share: the query heads of a kv head have one
-// list (that of the first). partials: decode_attn_partials() floats.
+// list (that of the first). ws: decode_attn_bytes() of workspace, 256-byte aligned.
 cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
-                               void* out, float* lse, float* partials, cudaStream_t st);
-size_t decode_attn_partials(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq,
-                            int kcap, bool share);
+                               void* out, float* lse, unsigned char* ws, cudaStream_t st);
+size_t decode_attn_bytes(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap,
+                         bool share);
 
 }  // namespace stem
