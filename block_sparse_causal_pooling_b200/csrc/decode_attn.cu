@@ -71,15 +71,22 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The same with the accumulator's first value given by column: D = A B + (c0, c1).
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], float c0, float c1, uint32_t a0,
-                                             uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                             uint32_t b1) {
+// The first of a chain: D = A B.
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%11,%10,%11};"
+      "{%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
   }
   float* o_s = reinterpret_cast<float*>(smem);  // [kWarps][8][D], over the rings at the end
   float qscale = kLog2e / sqrtf(static_cast<float>(D));  // of head g: logits in log2 units
-  float cinit[NG][2];
+  uint32_t ob0 = 0, ob1 = 0;  // B operand of the offsets' MMA (below)
   if constexpr (kQuant) {
     uint32_t top = 0;
 #pragma unroll
@@ -357,6 +364,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
                        : max(14 - (static_cast<int>(top >> 7) - 127), -100);
     qscale *= ldexpf(1.f, min(24 - up, 126));
     const float up1 = ldexpf(1.f, up / 2), up2 = ldexpf(1.f, up - up / 2);
+    float off[NG];
 #pragma unroll
     for (int y = 0; y < NG; ++y) {
       float sum = 0.f;
@@ -373,16 +381,32 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
       }
       sum += __shfl_xor_sync(kFull, sum, 1);
       sum += __shfl_xor_sync(kFull, sum, 2);
-      sum *= -static_cast<float>(L::OFFSET) * 0x1p-24f;
-      cinit[y][0] = __shfl_sync(kFull, sum, 8 * t);      // head 2t: lane row 2t
-      cinit[y][1] = __shfl_sync(kFull, sum, 8 * t + 4);  // head 2t + 1
+      off[y] = -static_cast<float>(L::OFFSET) * 0x1p-24f * sum;
     }
+    // What the codes' offset adds to a logit, sum_y s_ty off_yh, is one MMA of the scales as they
+    // are (bf16) with off in three bf16 pieces along k: groups (0, 1), (2, 3) or, of 64 channels,
+    // (0, 1) alone, from lane t = 0 on.
+    const int piece = NG == 4 ? t / 2 : t;
+    auto pieces = [&](float x, float& hi, float& mid, float& lo) {
+      hi = low16(pack_bf16(x, 0.f));
+      mid = low16(pack_bf16(x - hi, 0.f));
+      lo = x - hi - mid;
+    };
+    float h0_, m0_, l0_, h1_, m1_, l1_;
+    pieces(NG == 4 && (t & 1) ? off[NG - 2] : off[0], h0_, m0_, l0_);
+    pieces(NG == 4 && (t & 1) ? off[NG - 1] : off[1], h1_, m1_, l1_);
+    ob0 = piece == 0   ? pack_bf16(h0_, h1_)
+          : piece == 1 ? pack_bf16(m0_, m1_)
+          : piece == 2 ? pack_bf16(l0_, l1_)
+                       : 0u;
+    ob1 = NG == 4 && t < 2 ? pack_bf16(l0_, l1_) : 0u;
   }
   const float qs0 = __shfl_sync(kFull, qscale, 8 * t), qs1 = __shfl_sync(kFull, qscale, 8 * t + 4);
 
   float acc[2 * NG][4];  // rows: channels; columns: heads 2t, 2t + 1
   float asum[4];         // row y: sum of group y's weights
   float m0, m1, l0, l1;  // running maximum (log2 units) and sum of the weights as the MMA sees them
+  float lim0, lim1;      // largest logits (as the MMA gives them) within the maximum's slack
   float x0, x1;          // at 16 bits: sum of the weights before rounding
   float vf;              // power of two of the V scales
   int vlim;              // largest scale (bf16 bits) that vf is good for
@@ -399,7 +423,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
       for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) asum[e] = 0.f;
-    m0 = m1 = -INFINITY;
+    m0 = m1 = lim0 = lim1 = -INFINITY;
     l0 = l1 = x0 = x1 = 0.f;
     vf = 1.f;
     vlim = -1;
@@ -408,39 +432,50 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
     const int n_now = min(n_ent - e0, kStaged);
     for (int n = tid; n < n_now; n += kWarps * 32) ent[n] = list[e0 + n];
     __syncthreads();
-    const int units = n_now << spb_log;
-
-    // tokens of step u that are there, 0 or less where there is nothing to do
-    auto tokens = [&](int u, const Entry& e) -> int {
-      if (!(e.what >> 16 & heads)) return 0;
-      return len - static_cast<int>(e.what & 0xffffu) * a.c.block -
-             (u & ((1 << spb_log) - 1)) * C::STEP;
+    // Warp w takes steps [u0, u1) of the staged entries, one after the other: two walkers, one
+    // that fetches and one that computes, look at an entry when they come to it.
+    const int units = n_now << spb_log, per_entry = 1 << spb_log;
+    const int u0 = units * warp / kWarps, u1 = units * (warp + 1) / kWarps;
+    auto tokens = [&](const Entry& e) -> int {  // of an entry; 0 or less: nothing to do
+      return e.what >> 16 & heads ? len - static_cast<int>(e.what & 0xffffu) * a.c.block : 0;
     };
-    auto fetch = [&](int u, int stage) {
-      if (u < units) {
-        const Entry e = ent[u >> spb_log];
-        if (tokens(u, e) > 0) {
-          const unsigned char* src =
-              head_pages + e.page * page_bytes + (u & ((1 << spb_log) - 1)) * C::STEP_BYTES;
+    int fu = u0, ftok = 0;
+    const unsigned char* fsrc = nullptr;
+    auto fetch = [&](int stage) {
+      if (fu < u1) {
+        if (fu == u0 || (fu & (per_entry - 1)) == 0) {
+          const Entry e = ent[fu >> spb_log];
+          const int skip = fu & (per_entry - 1);
+          ftok = tokens(e) - skip * C::STEP;
+          fsrc = head_pages + e.page * page_bytes + skip * C::STEP_BYTES;
+        }
+        if (ftok > 0) {
           unsigned char* dst = ring + stage * C::STEP_BYTES + lane * 16;
 #pragma unroll
-          for (int n = 0; n < C::STEP_BYTES / 512; ++n) cp16(dst + n * 512, src + n * 512);
+          for (int n = 0; n < C::STEP_BYTES / 512; ++n) cp16(dst + n * 512, fsrc + n * 512);
           if (C::STEP_BYTES % 512 != 0 && lane < C::STEP_BYTES % 512 / 16)
-            cp16(dst + C::STEP_BYTES / 512 * 512, src + C::STEP_BYTES / 512 * 512);
+            cp16(dst + C::STEP_BYTES / 512 * 512, fsrc + C::STEP_BYTES / 512 * 512);
         }
+        ftok -= C::STEP;
+        fsrc += C::STEP_BYTES;
+        ++fu;
       }
       cp_commit();
     };
 #pragma unroll
-    for (int n = 0; n < C::STAGES - 1; ++n) fetch(warp + n * kWarps, n);
-    int stage = 0;
-    for (int u = warp; u < units; u += kWarps) {
+    for (int n = 0; n < C::STAGES - 1; ++n) fetch(n);
+    int stage = 0, valid = 0;
+    uint32_t hb = 0;
+    for (int u = u0; u < u1; ++u) {
       // the next step to fetch takes the stage that the step before this one has left
-      fetch(u + (C::STAGES - 1) * kWarps, stage == 0 ? C::STAGES - 1 : stage - 1);
+      fetch(stage == 0 ? C::STAGES - 1 : stage - 1);
       cp_wait<C::STAGES - 1>();
       __syncwarp();
-      const Entry e = ent[u >> spb_log];
-      const int valid = tokens(u, e);
+      if (u == u0 || (u & (per_entry - 1)) == 0) {
+        const Entry e = ent[u >> spb_log];
+        valid = tokens(e) - (u & (per_entry - 1)) * C::STEP;
+        hb = e.what >> 16 & heads;
+      }
       if (valid > 0) {
         const unsigned char* step = ring + stage * C::STEP_BYTES;
         // ---- logits: rows are tokens g and g + 8 of a tile, columns heads 2t and 2t + 1
@@ -449,14 +484,15 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
 #pragma unroll
         for (int i = 0; i < TPS; ++i) {
           const unsigned char* tile = step + i * L::TILE_BYTES;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) z[i][n] = 0.f;
           if constexpr (!kQuant) {
 #pragma unroll
             for (int y = 0; y < NG; ++y) {
               const uint4 ka = *reinterpret_cast<const uint4*>(tile + L::word(0, y, 0, lane));
               const uint4 kb = *reinterpret_cast<const uint4*>(tile + L::word(1, y, 0, lane));
-              mma_bf16(z[i], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
+              if (y == 0)
+                mma_bf16_new(z[i], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
+              else
+                mma_bf16(z[i], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
               mma_bf16(z[i], ka.z, kb.z, ka.w, kb.w, qf[y][2], qf[y][3]);
             }
           } else {
@@ -481,19 +517,24 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
                 sk[r][1] = sv[i][r][1] = 0;
               }
             }
+            {
+              const uint32_t s0 = NG == 4 && (t & 1) ? sk[0][1] : sk[0][0];
+              const uint32_t s1 = NG == 4 && (t & 1) ? sk[1][1] : sk[1][0];
+              mma_bf16_new(z[i], s0, s1, s0, s1, ob0, ob1);
+            }
 #pragma unroll
             for (int y = 0; y < NG; ++y) {
               float d[4];
               if constexpr (FMT == STEM_KV_Q4) {
                 const uint32_t a0 = kw[0][y], a1 = kw[1][y];
-                mma_f16_from(d, cinit[y][0], cinit[y][1], a0 & 0x000f000fu, a1 & 0x000f000fu,
+                mma_f16_new(d, a0 & 0x000f000fu, a1 & 0x000f000fu,
                              a0 & 0x00f000f0u, a1 & 0x00f000f0u, qf[y][0], qf[y][1]);
                 mma_f16(d, a0 >> 8 & 0x000f000fu, a1 >> 8 & 0x000f000fu, a0 >> 8 & 0x00f000f0u,
                         a1 >> 8 & 0x00f000f0u, qf[y][2], qf[y][3]);
               } else {
                 const uint32_t a0 = kw[0][2 * y], a1 = kw[1][2 * y];
                 const uint32_t b0 = kw[0][2 * y + 1], b1 = kw[1][2 * y + 1];
-                mma_f16_from(d, cinit[y][0], cinit[y][1], a0 & 0x00ff00ffu, a1 & 0x00ff00ffu,
+                mma_f16_new(d, a0 & 0x00ff00ffu, a1 & 0x00ff00ffu,
                              a0 >> 8 & 0x00ff00ffu, a1 >> 8 & 0x00ff00ffu, qf[y][0], qf[y][1]);
                 mma_f16(d, b0 & 0x00ff00ffu, b1 & 0x00ff00ffu, b0 >> 8 & 0x00ff00ffu,
                         b1 >> 8 & 0x00ff00ffu, qf[y][2], qf[y][3]);
@@ -506,12 +547,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
               z[i][3] = fmaf(s1, d[3], z[i][3]);
             }
           }
-#pragma unroll
-          for (int n = 0; n < 4; ++n) z[i][n] *= n & 1 ? qs1 : qs0;
         }
         // ---- tokens past the row's length and heads that do not keep the block: weight 0, and
         // scale 0, whatever their bytes hold
-        const uint32_t hb = e.what >> 16 & heads;
         if (valid < C::STEP || hb != 0xffu) {
           const bool on0 = hb >> (2 * t) & 1, on1 = hb >> (2 * t + 1) & 1;
 #pragma unroll
@@ -537,8 +575,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
                                          __vmaxu2(sv[1][0][1], sv[1][1][1])));
           move = static_cast<int>(max(top & 0xffffu, top >> 16)) > vlim;
         }
-        move |= n0 > m0 + kSlack || n1 > m1 + kSlack;
+        move |= n0 > lim0 || n1 > lim1;
         if (__any_sync(kFull, move)) {
+          n0 *= qs0;
+          n1 *= qs1;
 #pragma unroll
           for (int o = 4; o < 32; o *= 2) {
             n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, o));
@@ -550,10 +590,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
           const float a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
           m0 = n0;
           m1 = n1;
+          lim0 = (n0 + kSlack) * (1.f / qs0);
+          lim1 = (n1 + kSlack) * (1.f / qs1);
           l0 *= a0;
           l1 *= a1;
-          x0 *= a0;
-          x1 *= a1;
+          if constexpr (!kQuant) x0 *= a0, x1 *= a1;
           float c0 = a0, c1 = a1;
           if constexpr (kQuant) {
             uint32_t top = 0;  // largest finite scale: bf16 bits order like the numbers
@@ -591,64 +632,75 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
           asum[3] *= c1;
         }
         const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+        float p[TPS][4];
 #pragma unroll
         for (int i = 0; i < TPS; ++i) {
-          float p[4] = {ex2(z[i][0] - b0), ex2(z[i][1] - b1), ex2(z[i][2] - b0),
-                        ex2(z[i][3] - b1)};
-          const unsigned char* vt = step + i * L::TILE_BYTES + L::CODES;
-          if constexpr (!kQuant) {
-            x0 += p[0] + p[2];
-            x1 += p[1] + p[3];
-            const uint32_t pa = pack_bf16(p[0], p[1]), pb = pack_bf16(p[2], p[3]);
-            l0 += low16(pa) + low16(pb);
-            l1 += high16(pa) + high16(pb);
-            const uint32_t w0 = transpose8(pa), w1 = transpose8(pb);
-            if (valid >= kKvTile) {
+          p[i][0] = ex2(fmaf(z[i][0], qs0, -b0));
+          p[i][1] = ex2(fmaf(z[i][1], qs1, -b1));
+          p[i][2] = ex2(fmaf(z[i][2], qs0, -b0));
+          p[i][3] = ex2(fmaf(z[i][3], qs1, -b1));
+        }
+        // ---- O^T += V^T P: rows are channels, P^T is P transposed in registers
+        if constexpr (!kQuant) {
+          const unsigned char* vt = step + L::CODES;
+          x0 += p[0][0] + p[0][2];
+          x1 += p[0][1] + p[0][3];
+          const uint32_t pa = pack_bf16(p[0][0], p[0][1]), pb = pack_bf16(p[0][2], p[0][3]);
+          l0 += low16(pa) + low16(pb);
+          l1 += high16(pa) + high16(pb);
+          const uint32_t w0 = transpose8(pa), w1 = transpose8(pb);
+          if (valid >= kKvTile) {
 #pragma unroll
-              for (int y = 0; y < NG; ++y) {
-                const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
-                const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
-                mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, w0, w1);
-                mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, w0, w1);
-              }
-            } else {
-              // V rows of tokens that are not there may hold anything: 0 * NaN is not 0
-              const uint32_t ka = (2 * t < valid ? 0xffffu : 0u) |
-                                  (2 * t + 1 < valid ? 0xffff0000u : 0u);
-              const uint32_t kb = (2 * t + 8 < valid ? 0xffffu : 0u) |
-                                  (2 * t + 9 < valid ? 0xffff0000u : 0u);
-#pragma unroll
-              for (int y = 0; y < NG; ++y) {
-                const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
-                const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
-                mma_bf16(acc[2 * y], va.x & ka, va.y & ka, vb.x & kb, vb.y & kb, w0, w1);
-                mma_bf16(acc[2 * y + 1], va.z & ka, va.w & ka, vb.z & kb, vb.w & kb, w0, w1);
-              }
+            for (int y = 0; y < NG; ++y) {
+              const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
+              const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
+              mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, w0, w1);
+              mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, w0, w1);
             }
           } else {
-            l0 += p[0] + p[2];
-            l1 += p[1] + p[3];
+            // V rows of tokens that are not there may hold anything: 0 * NaN is not 0
+            const uint32_t ka = (2 * t < valid ? 0xffffu : 0u) |
+                                (2 * t + 1 < valid ? 0xffff0000u : 0u);
+            const uint32_t kb = (2 * t + 8 < valid ? 0xffffu : 0u) |
+                                (2 * t + 9 < valid ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) p[n] *= vf;
-            uint32_t vw[2][NG * L::WPG];
+            for (int y = 0; y < NG; ++y) {
+              const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
+              const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
+              mma_bf16(acc[2 * y], va.x & ka, va.y & ka, vb.x & kb, vb.y & kb, w0, w1);
+              mma_bf16(acc[2 * y + 1], va.z & ka, va.w & ka, vb.z & kb, vb.w & kb, w0, w1);
+            }
+          }
+        } else {
+          uint32_t vw[TPS][2][NG * L::WPG];
+#pragma unroll
+          for (int i = 0; i < TPS; ++i) {
+            l0 += p[i][0] + p[i][2];
+            l1 += p[i][1] + p[i][3];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) p[i][n] *= vf;
 #pragma unroll
             for (int q = 0; q < L::PIECES; ++q) {
-              const uint4 x = *reinterpret_cast<const uint4*>(vt + q * 512 + lane * 16);
+              const uint4 x = *reinterpret_cast<const uint4*>(step + i * L::TILE_BYTES + L::CODES +
+                                                              q * 512 + lane * 16);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int n = 0; n < 4; ++n)
-                vw[(q * 4 + n) / (NG * L::WPG)][(q * 4 + n) % (NG * L::WPG)] = w[n];
+                vw[i][(q * 4 + n) / (NG * L::WPG)][(q * 4 + n) % (NG * L::WPG)] = w[n];
             }
+          }
 #pragma unroll
-            for (int y = 0; y < NG; ++y) {
+          for (int y = 0; y < NG; ++y) {
+            const uint32_t one = g == y ? 0x3c003c00u : 0u;
+#pragma unroll
+            for (int i = 0; i < TPS; ++i) {
               const float s0 = y & 1 ? high16(sv[i][0][y / 2]) : low16(sv[i][0][y / 2]);
               const float s1 = y & 1 ? high16(sv[i][1][y / 2]) : low16(sv[i][1][y / 2]);
-              const uint32_t w0 = transpose8(pack_f16(p[0] * s0, p[1] * s0));
-              const uint32_t w1 = transpose8(pack_f16(p[2] * s1, p[3] * s1));
-              const uint32_t one = g == y ? 0x3c003c00u : 0u;
+              const uint32_t w0 = transpose8(pack_f16(p[i][0] * s0, p[i][1] * s0));
+              const uint32_t w1 = transpose8(pack_f16(p[i][2] * s1, p[i][3] * s1));
               mma_f16(asum, one, 0u, one, 0u, w0, w1);
               if constexpr (FMT == STEM_KV_Q4) {
-                const uint32_t va = vw[0][y], vb = vw[1][y];
+                const uint32_t va = vw[i][0][y], vb = vw[i][1][y];
                 mma_f16(acc[2 * y], va & 0x000f000fu, va & 0x00f000f0u, vb & 0x000f000fu,
                         vb & 0x00f000f0u, w0, w1);
                 mma_f16(acc[2 * y + 1], va >> 8 & 0x000f000fu, va >> 8 & 0x00f000f0u,
@@ -656,7 +708,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
               } else {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const uint32_t va = vw[0][2 * y + x], vb = vw[1][2 * y + x];
+                  const uint32_t va = vw[i][0][2 * y + x], vb = vw[i][1][2 * y + x];
                   mma_f16(acc[2 * y + x], va & 0x00ff00ffu, va >> 8 & 0x00ff00ffu,
                           vb & 0x00ff00ffu, vb >> 8 & 0x00ff00ffu, w0, w1);
                 }
@@ -666,6 +718,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
         }
       }
       __syncwarp();
+      valid -= C::STEP;
       stage = stage + 1 == C::STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
