@@ -93,26 +93,16 @@ int cache_rows(bool write, const stem_cache_t* c, void* k, void* v, int dtype, i
 
 // ------------------------------------------------------------------ decode
 
-struct Layout {
-  size_t scores = 0, attn = 0, total = 0;
-};
-
-// The attention's part depends on whether heads share lists: the larger of the two is reserved, so
-// that one size serves every method.
-Layout layout(const stem_cache_t* c, int R, int Hq, int kcap) {
-  Layout L;
-  size_t o = 0;
-  L.scores = o;
-  o += align_up(sizeof(double) * static_cast<size_t>(R) * Hq * c->max_blocks);
-  L.attn = o;
-  size_t most = 0;
+// The workspace depends on whether heads share lists: the larger of the two, so that one size
+// serves every method.
+size_t workspace(const stem_cache_t* c, int R, int Hq, int kcap) {
+  size_t most = kAlign;
   for (int share = 0; share < 2; ++share) {
     const size_t n = decode_attn_bytes(c->format, c->D, c->Hkv, c->max_blocks, R, Hq, kcap,
                                        share != 0);
     if (n > most) most = n;
   }
-  L.total = o + align_up(most);
-  return L;
+  return align_up(most);
 }
 
 int check_shape(const stem_cache_t* c, int R, int Hq, int kcap) {
@@ -153,8 +143,8 @@ int check_decode(const stem_decode_args_t* a, bool select, bool attend) {
     return STEM_ERR_ARG;
   if (select && (!a->budget || !aligned(a->budget, 4))) return STEM_ERR_ARG;
   if (attend && (!a->out || !aligned(a->out, 16) || !aligned(a->lse, 4))) return STEM_ERR_ARG;
-  const Layout L = layout(a->cache, a->R, a->Hq, a->kcap);
-  if (a->workspace == nullptr || !aligned(a->workspace, kAlign) || a->workspace_bytes < L.total)
+  if (a->workspace == nullptr || !aligned(a->workspace, kAlign) ||
+      a->workspace_bytes < workspace(a->cache, a->R, a->Hq, a->kcap))
     return STEM_ERR_WORKSPACE;
   return STEM_OK;
 }
@@ -162,7 +152,6 @@ int check_decode(const stem_decode_args_t* a, bool select, bool attend) {
 int run_decode(const stem_decode_args_t* a, bool select, bool attend, cudaStream_t st) {
   int rc = check_decode(a, select, attend);
   if (rc != STEM_OK) return rc == 1 ? STEM_OK : rc;
-  const Layout L = layout(a->cache, a->R, a->Hq, a->kcap);
   auto* ws = static_cast<unsigned char*>(a->workspace);
   const KvCache c = device_cache(a->cache);
   const DecodeRows r{a->q,    a->R,       a->Hq,      a->rows,  a->lens,
@@ -175,13 +164,14 @@ int run_decode(const stem_decode_args_t* a, bool select, bool attend, cudaStream
     m.beta = a->method->beta;
     m.clamp = a->method->clamp != 0;
     m.group = share;
-    rc = cuda_err(launch_decode_select(c, a->cache->D, r, a->budget, m,
-                                       reinterpret_cast<double*>(ws + L.scores), st));
+    DecodeLists lists;  // with the attention to follow, the selection leaves its lists
+    if (attend) lists = decode_lists(c, a->cache->format, a->cache->D, r, share, ws);
+    rc = cuda_err(launch_decode_select(c, a->cache->D, r, a->budget, m, lists, st));
     if (rc != STEM_OK) return rc;
   }
   if (!attend) return STEM_OK;
-  return cuda_err(launch_decode_attn(c, a->cache->format, a->cache->D, r, share, a->out, a->lse,
-                                     ws + L.attn, st));
+  return cuda_err(launch_decode_attn(c, a->cache->format, a->cache->D, r, share, select, a->out,
+                                     a->lse, ws, st));
 }
 
 }  // namespace
@@ -212,7 +202,7 @@ int stem_cache_read(const stem_cache_t* c, void* k, void* v, int dtype, int T,
 
 size_t stem_decode_workspace_size(const stem_cache_t* c, int R, int Hq, int kcap) {
   if (check_shape(c, R, Hq, kcap) != STEM_OK || R == 0) return 0;
-  return layout(c, R, Hq, kcap).total;
+  return workspace(c, R, Hq, kcap);
 }
 
 int stem_decode_select(const stem_decode_args_t* a, void* stream) {

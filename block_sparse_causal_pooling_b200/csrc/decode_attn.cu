@@ -33,6 +33,7 @@
 
 #include <algorithm>
 
+#include "decode_launch.h"
 #include "decode_rows.cuh"
 
 namespace stem {
@@ -40,7 +41,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4;
-constexpr int kHeadTile = 8;
+constexpr int kHeadTile = kDecodeHeads;
 constexpr int kStaged = 128;  // list entries in shared memory at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -129,27 +130,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float low16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// An entry of a list: the block's page, the block | query heads that keep it << 16.
-struct Entry {
-  int page;
-  uint32_t what;
-};
-__device__ __forceinline__ Entry entry_of(const KvCache& c, int seq, int j, uint32_t heads,
-                                          int32_t* status) {
-  const int page = kv_page(c, seq, j, status);
-  return page < 0 ? Entry{0, 0u} : Entry{page, static_cast<uint32_t>(j) | heads << 16};
-}
-
 struct Args {
   KvCache c;
   DecodeRows r;
   bool share;
-  int tiles_h;  // head tiles of a kv head
-  int items;    // R * Hkv * tiles_h: a row, a kv head and up to 8 of its query heads
-  int most;     // entries a list may have
-  // One list of blocks for each (row, kv head) where its heads share it, else for each item.
-  Entry* list;     // [lists][most]
-  int32_t* count;  // [lists]
+  DecodeLists lists;
+  int items;  // R * Hkv * lists.tiles_h: a row, a kv head and up to 8 of its query heads
   // Entry numbers run over the items in order; CTA n of N = min(ctas, total) takes total * n / N and
   // up (at least one).
   int ctas;
@@ -173,14 +159,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
   __shared__ uint32_t wbuf[kPlanThreads / 32];
   const int tid = threadIdx.x, row = blockIdx.y, G = a.r.Hq / a.c.Hkv;
   const int64_t list = static_cast<int64_t>(row) * gridDim.x + blockIdx.x;
-  Entry* out = a.list + list * a.most;
+  Entry* out = a.lists.list + list * a.lists.most;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
   int seq, len;
   decode_row(a.c, a.r, row, seq, len);
   const int last = (len + a.c.block - 1) / a.c.block - 1;
   if (last < 0) {
-    if (tid == 0) a.count[list] = 0;
+    if (tid == 0) a.lists.count[list] = 0;
     return;
   }
   if (a.share) {
@@ -197,16 +183,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
         out[e] = Entry{0, 0u};
       }
     }
-    if (tid == 0) a.count[list] = n;
+    if (tid == 0) a.lists.count[list] = n;
     return;
   }
   // the union of the heads' lists, in block order
-  const int kv = blockIdx.x / a.tiles_h, h0 = blockIdx.x % a.tiles_h * kHeadTile;
+  const int kv = blockIdx.x / a.lists.tiles_h, h0 = blockIdx.x % a.lists.tiles_h * kHeadTile;
   const int nh = min(G - h0, kHeadTile);
-  const uint32_t none = 0xffu << nh & 0xffu;  // columns without a head go along with any block
   const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
-  const int words = (last + 4) / 4;
-  for (int w = tid; w < words; w += kPlanThreads) mask[w] = 0;
+  for (int w = tid; w < last / 4 + 1; w += kPlanThreads) mask[w] = 0;
   __syncthreads();
   for (int n = tid; n < nh * a.r.kcap; n += kPlanThreads) {
     const int h = n / a.r.kcap, e = n % a.r.kcap;
@@ -220,36 +204,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
       *a.r.status = STEM_ERR_ARG;
   }
   __syncthreads();
-  const int run = (words + kPlanThreads - 1) / kPlanThreads;  // thread t owns a run of words
-  const int w0 = min(tid * run, words), w1 = min(w0 + run, words);
-  uint32_t n = 0;
-  for (int w = w0; w < w1; ++w)
-    for (int b = 0; b < 4; ++b) n += (mask[w] >> (8 * b) & 0xffu) != 0;
-  uint32_t s = n;
-  for (int o = 1; o < 32; o *= 2) {
-    const uint32_t y = __shfl_up_sync(kFull, s, o);
-    if (tid % 32 >= o) s += y;
-  }
-  if (tid % 32 == 31) wbuf[tid / 32] = s;
-  __syncthreads();
-  uint32_t total = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < tid / 32) s += wbuf[w];
-    total += wbuf[w];
-  }
-  uint32_t at = s - n;
-  for (int w = w0; w < w1; ++w)
-    for (int b = 0; b < 4; ++b) {
-      const uint32_t m = mask[w] >> (8 * b) & 0xffu;
-      if (m) out[at++] = entry_of(a.c, seq, 4 * w + b, m | none, a.r.status);
-    }
-  if (tid == 0) a.count[list] = static_cast<int32_t>(total);
+  write_union<kPlanThreads>(a.c, a.lists, list, seq, last, nh, mask, wbuf, a.r.status);
 }
 
 // ------------------------------------------------------------------ attention
 
 __device__ __forceinline__ int list_of(const Args& a, int item) {
-  return a.share ? item / a.tiles_h : item;
+  return a.share ? item / a.lists.tiles_h : item;
 }
 
 // Where a CTA starts: the total number of entries, and the item and the entry in it that its first
@@ -263,7 +224,7 @@ __device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int64_t* ws
   const int tid = threadIdx.x, run = (a.items + kWarps * 32 - 1) / (kWarps * 32);
   const int i0 = min(tid * run, a.items), i1 = min(i0 + run, a.items);
   int64_t n = 0;
-  for (int i = i0; i < i1; ++i) n += a.count[list_of(a, i)];
+  for (int i = i0; i < i1; ++i) n += a.lists.count[list_of(a, i)];
   int64_t s = n;
   for (int o = 1; o < 32; o *= 2) {
     const int64_t y = __shfl_up_sync(kFull, s, o);
@@ -281,7 +242,7 @@ __device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int64_t* ws
   if (blockIdx.x < total && first >= s && first < s + n) {
     int i = i0;
     for (;; ++i) {
-      const int c = a.count[list_of(a, i)];
+      const int c = a.lists.count[list_of(a, i)];
       if (first < s + c) break;
       s += c;
     }
@@ -319,16 +280,16 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
 
   // this CTA's part of one item after the other
   for (; e_at < e_end; ++item, entry = 0) {
-  const int n_item = a.count[list_of(a, item)];
+  const int n_item = a.lists.count[list_of(a, item)];
   const int n_ent = static_cast<int>(min(static_cast<int64_t>(n_item - entry), e_end - e_at));
   if (n_ent <= 0) continue;
   const bool whole = n_ent == n_item;
   const int slot = 2 * blockIdx.x + (e_at == e_first ? 0 : 1);
   if (entry == 0 && tid == 0) a.start[item] = e_at;
   e_at += n_ent;
-  const Entry* list = a.list + static_cast<int64_t>(list_of(a, item)) * a.most + entry;
-  const int row = item / (a.c.Hkv * a.tiles_h), kv = item / a.tiles_h % a.c.Hkv;
-  const int h0 = item % a.tiles_h * kHeadTile;
+  const Entry* list = a.lists.list + static_cast<int64_t>(list_of(a, item)) * a.lists.most + entry;
+  const int row = item / (a.c.Hkv * a.lists.tiles_h), kv = item / a.lists.tiles_h % a.c.Hkv;
+  const int h0 = item % a.lists.tiles_h * kHeadTile;
   const int nh = min(G - h0, kHeadTile);
   const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
   int seq, len;
@@ -835,11 +796,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps], s_o[kGroups][D];
   const int row = blockIdx.y, head = blockIdx.x, tid = threadIdx.x;
   const int G = a.r.Hq / a.c.Hkv, h = head % G % kHeadTile;
-  const int item = (row * a.c.Hkv + head / G) * a.tiles_h + head % G / kHeadTile;
+  const int item = (row * a.c.Hkv + head / G) * a.lists.tiles_h + head % G / kHeadTile;
   const int64_t o_at = static_cast<int64_t>(row) * a.r.Hq + head;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
-  const int n = a.count[list_of(a, item)];
+  const int n = a.lists.count[list_of(a, item)];
   if (n == 0) {
     if (tid < D) a.out[o_at * D + tid] = __float2bfloat16_rn(0.f);
     if (tid == 0 && a.lse) a.lse[o_at] = -INFINITY;
@@ -931,57 +892,51 @@ Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kc
   return s;
 }
 
-// Launches on a stream whose previous kernel may still be running: the kernels wait for it
-// themselves (cudaGridDependencySynchronize), after they have been set up.
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
-                         const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int FMT, int D>
-cudaError_t launch(const Args& a, cudaStream_t st) {
+cudaError_t launch(const Args& a, bool planned, cudaStream_t st) {
   using C = Cfg<FMT, D>;
   static_assert(C::RING >= kHeadTile * D * 4, "the rings hold the warps' results at the end");
-  const size_t mask = a.share ? 0 : 4 * ((a.c.max_blocks + 3) / 4);
-  cudaError_t e = launch_after(
-      plan_kernel, dim3(a.share ? a.c.Hkv : a.c.Hkv * a.tiles_h, a.r.R), kPlanThreads, mask, st, a);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (!planned) {
+    const size_t mask = a.share ? 0 : 4 * ((a.c.max_blocks + 3) / 4);
+    const int lists = a.share ? a.c.Hkv : a.c.Hkv * a.lists.tiles_h;
+    e = launch_after(plan_kernel, dim3(lists, a.r.R), kPlanThreads, mask, 1, st, a);
+    if (e != cudaSuccess) return e;
+  }
   constexpr size_t bytes = static_cast<size_t>(kWarps) * C::RING;
   // the attribute is per device; setting it is cheap and idempotent
   e = cudaFuncSetAttribute(attn_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  e = launch_after(attn_kernel<FMT, D>, dim3(a.ctas), kWarps * 32, bytes, st, a);
+  e = launch_after(attn_kernel<FMT, D>, dim3(a.ctas), kWarps * 32, bytes, 1, st, a);
   if (e != cudaSuccess) return e;
   return launch_after(join_kernel<D>, dim3(a.r.Hq, a.r.R), kJoinThreads, sizeof(float) * a.ctas,
-                      st, a);
+                      1, st, a);
 }
 
 }  // namespace
 
+DecodeLists decode_lists(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
+                         unsigned char* ws) {
+  const Sizes s = sizes_of(format, D, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
+  DecodeLists l;
+  l.list = reinterpret_cast<Entry*>(ws + s.list);
+  l.count = reinterpret_cast<int32_t*>(ws + s.count);
+  l.most = s.most;
+  l.tiles_h = s.tiles_h;
+  return l;
+}
+
 cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
-                               void* out, float* lse, unsigned char* ws, cudaStream_t st) {
+                               bool planned, void* out, float* lse, unsigned char* ws,
+                               cudaStream_t st) {
   const Sizes s = sizes_of(format, D, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
   Args a;
   a.c = c;
   a.r = r;
   a.share = share;
-  a.tiles_h = s.tiles_h;
+  a.lists = decode_lists(c, format, D, r, share, ws);
   a.items = static_cast<int>(s.items);
-  a.most = s.most;
-  a.list = reinterpret_cast<Entry*>(ws + s.list);
-  a.count = reinterpret_cast<int32_t*>(ws + s.count);
   a.ctas = s.ctas;
   a.start = reinterpret_cast<int64_t*>(ws + s.start);
   a.out = static_cast<__nv_bfloat16*>(out);
@@ -990,15 +945,15 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   a.part = reinterpret_cast<float*>(ws + s.part);
   if (D == 128) {
     switch (format) {
-      case STEM_KV_BF16: return launch<STEM_KV_BF16, 128>(a, st);
-      case STEM_KV_Q8: return launch<STEM_KV_Q8, 128>(a, st);
-      default: return launch<STEM_KV_Q4, 128>(a, st);
+      case STEM_KV_BF16: return launch<STEM_KV_BF16, 128>(a, planned, st);
+      case STEM_KV_Q8: return launch<STEM_KV_Q8, 128>(a, planned, st);
+      default: return launch<STEM_KV_Q4, 128>(a, planned, st);
     }
   }
   switch (format) {
-    case STEM_KV_BF16: return launch<STEM_KV_BF16, 64>(a, st);
-    case STEM_KV_Q8: return launch<STEM_KV_Q8, 64>(a, st);
-    default: return launch<STEM_KV_Q4, 64>(a, st);
+    case STEM_KV_BF16: return launch<STEM_KV_BF16, 64>(a, planned, st);
+    case STEM_KV_Q8: return launch<STEM_KV_Q8, 64>(a, planned, st);
+    default: return launch<STEM_KV_Q4, 64>(a, planned, st);
   }
 }
 

@@ -30,15 +30,36 @@ struct DecodeRows {
   int32_t* status;
 };
 
-// Block scores and selection (decode_select.cu). scores: R * Hq * max_blocks doubles.
+// An entry of the attention's lists: the block's page, the block | query heads that keep it << 16.
+struct Entry {
+  int page;
+  uint32_t what;
+};
+constexpr int kDecodeHeads = 8;  // query heads of an item (columns of an MMA)
+
+// One list of blocks for each (row, kv head) where its heads share it, else for each item (row, kv
+// head, 8 of its query heads): [lists][most] and [lists].
+struct DecodeLists {
+  Entry* list = nullptr;
+  int32_t* count = nullptr;
+  int most = 0;
+  int tiles_h = 0;  // items of a kv head
+};
+
+// Block scores and selection (decode_select.cu); writes the attention's lists too where lists.list
+// is not NULL.
 cudaError_t launch_decode_select(const KvCache& c, int D, const DecodeRows& r,
-                                 const int32_t* budget, SelMetric metric, double* scores,
+                                 const int32_t* budget, SelMetric metric, const DecodeLists& lists,
                                  cudaStream_t st);
 
 // Attention over the kept blocks (decode_attn.cu). share: the query heads of a kv head have one
-// list (that of the first). ws: decode_attn_bytes() of workspace, 256-byte aligned.
+// list (that of the first). ws: decode_attn_bytes() of workspace, 256-byte aligned; planned: its
+// lists are there already.
+DecodeLists decode_lists(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
+                         unsigned char* ws);
 cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
-                               void* out, float* lse, unsigned char* ws, cudaStream_t st);
+                               bool planned, void* out, float* lse, unsigned char* ws,
+                               cudaStream_t st);
 size_t decode_attn_bytes(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap,
                          bool share);
 

@@ -21,4 +21,47 @@ __host__ __device__ __forceinline__ void decode_row(const KvCache& c, const Deco
   }
 }
 
+__device__ __forceinline__ Entry entry_of(const KvCache& c, int seq, int j, uint32_t heads,
+                                          int32_t* status) {
+  const int page = kv_page(c, seq, j, status);
+  return page < 0 ? Entry{0, 0u} : Entry{page, static_cast<uint32_t>(j) | heads << 16};
+}
+
+// The list of an item from its blocks' head bits, in block order: mask holds a byte for each of the
+// blocks 0 .. last (last < 0: none). Called by a CTA of THREADS threads; scan: THREADS / 32 words.
+template <int THREADS>
+__device__ __forceinline__ void write_union(const KvCache& c, const DecodeLists& lists,
+                                            int64_t item, int seq, int last, int nh,
+                                            const uint32_t* mask, uint32_t* scan,
+                                            int32_t* status) {
+  const int tid = threadIdx.x, words = last < 0 ? 0 : last / 4 + 1;
+  const uint32_t none = 0xffu << nh & 0xffu;  // columns without a head go along with any block
+  const int run = (words + THREADS - 1) / THREADS;  // thread t owns a run of words
+  const int w0 = min(tid * run, words), w1 = min(w0 + run, words);
+  uint32_t n = 0;
+  for (int w = w0; w < w1; ++w)
+    for (int b = 0; b < 4; ++b) n += (mask[w] >> (8 * b) & 0xffu) != 0;
+  uint32_t s = n;
+  for (int o = 1; o < 32; o *= 2) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (tid % 32 >= o) s += y;
+  }
+  __syncthreads();
+  if (tid % 32 == 31) scan[tid / 32] = s;
+  __syncthreads();
+  uint32_t total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < tid / 32) s += scan[w];
+    total += scan[w];
+  }
+  uint32_t at = s - n;
+  Entry* out = lists.list + item * lists.most;
+  for (int w = w0; w < w1; ++w)
+    for (int b = 0; b < 4; ++b) {
+      const uint32_t m = mask[w] >> (8 * b) & 0xffu;
+      if (m) out[at++] = entry_of(c, seq, 4 * w + b, m | none, status);
+    }
+  if (tid == 0) lists.count[item] = static_cast<int32_t>(total);
+}
+
 }  // namespace stem

@@ -8,96 +8,34 @@
 // (k+1)-th blocks among a thousand can be closer than a float32 dot product is accurate, and the
 // choice is meant to be the definition's. The device has one double FMA for two float32 ones, so
 // this costs less than reading kbar: 2 G D flops a block and kv head against 4 D bytes.
+//
+// One cluster of up to 8 CTAs per (row, kv head), so that scores never leave shared memory and a
+// single launch does it all: each CTA scores a run of blocks for 8 heads at a time (a lane holds 16
+// channels of two blocks and meets them with one head after the other), the heads' softmax sums and
+// then the keys are exchanged through distributed shared memory, and each list is picked by one
+// CTA of the cluster. Latency bounds it for a few rows, reading kbar for many.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <cfloat>
+#include <algorithm>
 
+#include "decode_launch.h"
 #include "decode_rows.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace stem {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kScoreWarps = 8;
-constexpr int kScoreBlocks = 32;  // blocks a CTA scores
-constexpr int kPickThreads = 256;
-constexpr int kHeads = 4;  // query heads a warp scores at once
-
-// ------------------------------------------------------------------ scores
-
-// One warp per cached block: lane l holds channels (D/32) l .. of kbar and of kHeads queries; the
-// heads' partial sums are folded so that five shuffle steps reduce all of them.
-template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(KvCache c, DecodeRows r,
-                                                                 double* scores) {
-  constexpr int CH = D / 32;
-  const int row = blockIdx.z, kv = blockIdx.y, G = r.Hq / c.Hkv;
-  int seq, len;
-  decode_row(c, r, row, seq, len);
-  const int last = (len + c.block - 1) / c.block - 1;
-  const int j0 = blockIdx.x * kScoreBlocks, j1 = min(j0 + kScoreBlocks, last);
-  if (j0 >= j1) return;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const double scale = 1.0 / sqrt(static_cast<double>(D));
-  for (int h0 = 0; h0 < G; h0 += kHeads) {
-    double q[kHeads][CH];
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      const bool on = h0 + h < G;
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(r.q) +
-                               (static_cast<int64_t>(row) * r.Hq + kv * G + (on ? h0 + h : 0)) * D +
-                               lane * CH;
-#pragma unroll
-      for (int e = 0; e < CH; ++e) q[h][e] = on ? static_cast<double>(__bfloat162float(p[e])) : 0.0;
-    }
-    for (int j = j0 + warp; j < j1; j += kScoreWarps) {
-      const int page = kv_page(c, seq, j, r.status);
-      double s[kHeads];
-      float k[CH];
-      if (page >= 0) {
-        const float* kb = c.kbar + (static_cast<int64_t>(page) * c.Hkv + kv) * D + lane * CH;
-        if constexpr (CH == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(kb);
-          k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(kb);
-          k[0] = x.x, k[1] = x.y;
-        }
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          s[h] = 0.0;
-#pragma unroll
-          for (int e = 0; e < CH; ++e) s[h] = fma(q[h][e], static_cast<double>(k[e]), s[h]);
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) s[h] = -INFINITY;
-      }
-      // fold: after the first two steps lane l holds head (l & 1) * 2 + (l >> 1 & 1)
-      const bool up1 = lane & 1, up2 = lane & 2;
-      double a0 = up1 ? s[2] : s[0], a1 = up1 ? s[3] : s[1];
-      a0 += __shfl_xor_sync(kFull, up1 ? s[0] : s[2], 1);
-      a1 += __shfl_xor_sync(kFull, up1 ? s[1] : s[3], 1);
-      double t = up2 ? a1 : a0;
-      t += __shfl_xor_sync(kFull, up2 ? a0 : a1, 2);
-#pragma unroll
-      for (int o = 4; o < 32; o *= 2) t += __shfl_xor_sync(kFull, t, o);
-      const int h = (lane & 1) * 2 + (lane >> 1 & 1);
-      if (lane < kHeads && h0 + h < G)
-        scores[(static_cast<int64_t>(row) * r.Hq + kv * G + h0 + h) * c.max_blocks + j] = t * scale;
-    }
-  }
-}
-
-// ------------------------------------------------------------------ selection
-
-// Order-preserving map of a double to an unsigned integer; NaN ranks with -infinity, -0 with +0.
-__device__ __forceinline__ uint64_t rank_of(double x) {
-  x = isnan(x) ? -INFINITY : x + 0.0;
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x));
-  return b >> 63 ? ~b : b | 1ull << 63;
-}
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kHeads = kDecodeHeads;  // heads of a pass
+constexpr int kMaxCluster = 8;
+constexpr int kSlice = 64;      // a cluster grows to fill the device, but to no fewer blocks a CTA
+constexpr int kMaxSlice = 512;  // what a CTA's shared memory holds
+static_assert(kMaxCluster * kMaxSlice >= STEM_MAX_NB, "a cluster holds the longest context");
 
 // What a block's V magnitude adds to its key.
 __device__ __forceinline__ double magnitude(const SelMetric& m, float n) {
@@ -107,228 +45,489 @@ __device__ __forceinline__ double magnitude(const SelMetric& m, float n) {
   return static_cast<double>(m.beta) * (m.clamp && e < 0.0 ? 0.0 : e);
 }
 
-__device__ __forceinline__ double block_max(double x, double* buf) {
-  for (int o = 16; o; o /= 2) x = fmax(x, __shfl_xor_sync(kFull, x, o));
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = x;
-  __syncthreads();
-  x = buf[0];
-  for (int n = 1; n < kPickThreads / 32; ++n) x = fmax(x, buf[n]);
-  return x;
-}
-__device__ __forceinline__ double block_sum(double x, double* buf) {
-  for (int o = 16; o; o /= 2) x += __shfl_xor_sync(kFull, x, o);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = x;
-  __syncthreads();
-  x = buf[0];
-  for (int n = 1; n < kPickThreads / 32; ++n) x += buf[n];
-  return x;
-}
-// Exclusive prefix sum over the CTA's threads.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* buf) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  uint32_t s = x;
-  for (int o = 1; o < 32; o *= 2) {
-    const uint32_t y = __shfl_up_sync(kFull, s, o);
-    if (lane >= o) s += y;
-  }
-  __syncthreads();
-  if (lane == 31) buf[warp] = s;
-  __syncthreads();
-  uint32_t before = 0;
-  for (int n = 0; n < warp; ++n) before += buf[n];
-  return before + s - x;
+// Keys as they are compared: NaN ranks with -infinity, -0 with +0.
+__device__ __forceinline__ double as_key(double x) { return isnan(x) ? -INFINITY : x + 0.0; }
+// Order-preserving map of a key to an unsigned integer.
+__device__ __forceinline__ uint64_t rank_of(double x) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x));
+  return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-// One CTA per (row, list): keys of the candidates 1 .. i - 1 in shared memory, the k - 2 best by a
-// radix select from the first digit in which the keys differ, then the list in ascending order.
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(KvCache c, DecodeRows r,
-                                                            const int32_t* budget, SelMetric m,
-                                                            const double* scores) {
-  extern __shared__ uint64_t key[];  // max_blocks
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t wbuf[kPickThreads / 32];
-  __shared__ double dbuf[kPickThreads / 32];
-  __shared__ uint64_t s_lo, s_hi;
-  __shared__ uint32_t s_bin, s_need, s_cnt;
-  const int row = blockIdx.y, tid = threadIdx.x, G = r.Hq / c.Hkv;
-  const int per = m.group ? G : 1;  // heads that get this list
-  const int head = blockIdx.x * per, kv = head / G;
-  int seq, len;
-  decode_row(c, r, row, seq, len);
-  const int last = (len + c.block - 1) / c.block - 1;
-  int k = 0;
-  if (last >= 0) {
-    k = budget[last];
-    const int lo = min(last + 1, 2);
-    if (k < lo || k > last + 1 || k > r.kcap) {
-      if (r.status && tid == 0) *r.status = STEM_ERR_ARG;
-      k = min(max(k, lo), min(last + 1, r.kcap));
+// The threads that pick one list: a warp (of 8 that pick 8 lists at once) or the whole CTA.
+template <int T>
+struct Team {
+  static constexpr int kBuckets = T == 32 ? 256 : 1024;  // of the first cut of the keys
+  static constexpr int kTied = T == 32 ? 128 : 256;      // keys ranked one by one at most
+  double lo[T / 32], hi[T / 32];
+  double tied_key[kTied];
+  uint32_t hist[kBuckets];
+  uint32_t kept[STEM_MAX_NB / 32 + 1];  // bit j: block j is kept
+  uint32_t scan[T / 32];
+  uint32_t cut, need, found, tied;
+  uint16_t tied_at[kTied];
+
+  static __device__ __forceinline__ int tid() { return threadIdx.x % T; }
+  static __device__ __forceinline__ void sync() {
+    if (T == 32)
+      __syncwarp();
+    else
+      __syncthreads();
+  }
+  // Exclusive prefix sum over the team's threads.
+  __device__ __forceinline__ uint32_t prefix(uint32_t x) {
+    const int lane = threadIdx.x % 32, warp = tid() / 32;
+    uint32_t s = x;
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t y = __shfl_up_sync(kFull, s, o);
+      if (lane >= o) s += y;
+    }
+    if (T == 32) return s - x;
+    sync();
+    if (lane == 31) scan[warp] = s;
+    sync();
+    uint32_t before = 0;
+    for (int n = 0; n < warp; ++n) before += scan[n];
+    return before + s - x;
+  }
+  __device__ __forceinline__ uint32_t sum(uint32_t x) {
+    x = __reduce_add_sync(kFull, x);
+    if (T == 32) return x;
+    sync();
+    if (threadIdx.x % 32 == 0) scan[tid() / 32] = x;
+    sync();
+    x = 0;
+    for (int n = 0; n < T / 32; ++n) x += scan[n];
+    return x;
+  }
+};
+
+// The `want` best of the candidates 1 .. last - 1 by key, ties to the lower block, into s.kept
+// (beside the sink 0 and the diagonal block). One pass cuts the keys into equal intervals between
+// the smallest and the largest; the few of the interval at the cut are ranked one by one.
+template <int T>
+__device__ void pick(const double* key, int last, int want, Team<T>& s) {
+  const int tid = s.tid();
+  const int words = last / 32 + 1;
+  const bool all = want >= last - 1;  // (every block is kept)
+  for (int w = tid; w < words; w += T) {
+    uint32_t x = all ? kFull : w == 0 ? 1u : 0u;
+    if (w == last / 32) {
+      const int r = last % 32;
+      x = (x | 1u << r) & (r == 31 ? kFull : (2u << r) - 1u);
+    }
+    s.kept[w] = x;
+  }
+  if (all || want <= 0) {
+    s.sync();
+    return;
+  }
+  double lo = INFINITY, hi = -INFINITY;  // of the finite keys
+  for (int j = 1 + tid; j < last; j += T) {
+    const double x = key[j];
+    if (!isinf(x)) {
+      lo = fmin(lo, x);
+      hi = fmax(hi, x);
     }
   }
-  int32_t* out = r.sel_idx + (static_cast<int64_t>(row) * r.Hq + head) * r.kcap;
-  const int want = max(min(k, last + 1) - 2, 0);  // beside the sink and the diagonal block
-  const int ncand = max(last - 1, 0);
-  const bool all = want >= ncand;
-  uint64_t cut = 0;  // keys of at least cut (shifted) are in, but for ties at the cut
-  int shift = 0;
-  uint32_t ties = 0;  // how many of those equal to the cut
-  if (last > 1 && !all && want > 0) {
-    const double* s = scores + (static_cast<int64_t>(row) * r.Hq + head) * c.max_blocks;
-    double lse[8];
-    const bool product_group = m.group && !m.additive && G > 1;
-    uint64_t lo = ~0ull, hi = 0;
-    // the group's product metric needs each head's softmax denominator (8 heads at a time)
-    double* acc = reinterpret_cast<double*>(key);
-    if (product_group) {
-      for (int j = tid; j < last; j += kPickThreads) acc[j] = -INFINITY;
-      for (int h0 = 0; h0 < G; h0 += 8) {
-        const int nh = min(8, G - h0);
-        for (int h = 0; h < nh; ++h) {
-          const double* sh = s + static_cast<int64_t>(h0 + h) * c.max_blocks;
-          double top = -INFINITY, sum = 0.0;
-          for (int j = tid; j < last; j += kPickThreads) top = fmax(top, sh[j]);
-          top = block_max(top, dbuf);
-          if (!(top > -INFINITY)) top = 0.0;
-          for (int j = tid; j < last; j += kPickThreads) sum += exp(sh[j] - top);
-          lse[h] = top + log(block_sum(sum, dbuf));
-        }
-        for (int j = tid; j < last; j += kPickThreads) {
-          double top = acc[j];
-          for (int h = 0; h < nh; ++h)
-            top = fmax(top, s[static_cast<int64_t>(h0 + h) * c.max_blocks + j] - lse[h]);
-          double sum = 0.0;
-          if (top > -INFINITY) {
-            sum = exp(acc[j] - top);
-            for (int h = 0; h < nh; ++h)
-              sum += exp(s[static_cast<int64_t>(h0 + h) * c.max_blocks + j] - lse[h] - top);
-            acc[j] = top + log(sum);
-          }
-        }
+  for (int o = 16; o; o /= 2) {
+    lo = fmin(lo, __shfl_xor_sync(kFull, lo, o));
+    hi = fmax(hi, __shfl_xor_sync(kFull, hi, o));
+  }
+  for (int b = tid; b < s.kBuckets; b += T) s.hist[b] = 0;
+  if (tid % 32 == 0) s.lo[tid / 32] = lo, s.hi[tid / 32] = hi;
+  if (tid == 0) s.tied = 0;
+  s.sync();
+  for (int w = 0; w < T / 32; ++w) lo = fmin(lo, s.lo[w]), hi = fmax(hi, s.hi[w]);
+  // (a product that rounds keeps the order: a larger key never falls into a lower interval)
+  const double scale = hi > lo ? (s.kBuckets - 1) / (hi - lo) : 0.0;
+  auto bucket = [&](double x) -> int {
+    if (x == -INFINITY) return 0;
+    if (x == INFINITY) return s.kBuckets - 1;
+    return min(static_cast<int>((x - lo) * scale), s.kBuckets - 1);
+  };
+  for (int j = 1 + tid; j < last; j += T) atomicAdd(&s.hist[bucket(key[j])], 1u);
+  s.sync();
+  {
+    constexpr int kRun = Team<T>::kBuckets / T;  // thread t owns a run of buckets from the top down
+    uint32_t n = 0;
+    for (int i = 0; i < kRun; ++i) n += s.hist[s.kBuckets - 1 - (tid * kRun + i)];
+    uint32_t before = s.prefix(n);
+    for (int i = 0; i < kRun; ++i) {
+      const int b = s.kBuckets - 1 - (tid * kRun + i);
+      const uint32_t c = s.hist[b];
+      if (before < static_cast<uint32_t>(want) && before + c >= static_cast<uint32_t>(want)) {
+        s.cut = b;
+        s.need = want - before;
+        s.found = c;
       }
-    }
-    for (int j = tid; j < last; j += kPickThreads) {  // (as above: a block stays with its thread)
-      if (j == 0) continue;
-      const int page = kv_page(c, seq, j, r.status);
-      double x = -INFINITY;
-      if (page >= 0) {
-        const double w =
-            magnitude(m, c.vnorm[static_cast<int64_t>(page) * c.Hkv + kv]);
-        if (product_group) {
-          x = acc[j] + w;
-        } else {
-          x = 0.0;
-          for (int h = 0; h < per; ++h) x += s[static_cast<int64_t>(h) * c.max_blocks + j];
-          x += m.additive ? per * w : w;
-        }
-      }
-      const uint64_t u = rank_of(x);
-      key[j] = u;
-      lo = min(lo, u);
-      hi = max(hi, u);
-    }
-    if (tid == 0) s_lo = ~0ull, s_hi = 0;
-    __syncthreads();
-    for (int o = 16; o; o /= 2) {
-      lo = min(lo, __shfl_xor_sync(kFull, lo, o));
-      hi = max(hi, __shfl_xor_sync(kFull, hi, o));
-    }
-    if (tid % 32 == 0) {
-      atomicMin(reinterpret_cast<unsigned long long*>(&s_lo), lo);
-      atomicMax(reinterpret_cast<unsigned long long*>(&s_hi), hi);
-    }
-    __syncthreads();
-    lo = s_lo, hi = s_hi;
-    if (lo == hi) {
-      cut = hi;
-      ties = want;
-    } else {
-      // digits of 8 bits from the first differing bit down
-      int top = 64 - __clzll(lo ^ hi);  // bits [0, top) differ
-      uint64_t prefix = top == 64 ? 0 : hi >> top;
-      uint32_t need = want;
-      for (;;) {
-        const int bits = min(8, top);
-        shift = top - bits;
-        __syncthreads();
-        hist[tid] = 0;
-        __syncthreads();
-        for (int j = 1 + tid; j < last; j += kPickThreads) {
-          const uint64_t u = key[j];
-          if ((top == 64 ? 0 : u >> top) == prefix)
-            atomicAdd(&hist[u >> shift & ((1u << bits) - 1)], 1u);
-        }
-        __syncthreads();
-        // thread t owns bin 255 - t: keys in higher bins come before it
-        const uint32_t n = hist[255 - tid];
-        const uint32_t before = block_scan(n, wbuf);
-        if (before < need && before + n >= need) {
-          s_bin = 255 - tid;
-          s_need = need - before;
-          s_cnt = n;
-        }
-        __syncthreads();
-        prefix = prefix << bits | s_bin;
-        need = s_need;
-        top = shift;
-        if (s_cnt == need || top == 0) break;
-      }
-      cut = prefix;
-      ties = need;
+      before += c;
     }
   }
-  // ascending output: thread t owns a run of blocks
-  const int run = (last + 1 + kPickThreads - 1) / kPickThreads;
-  const int b0 = min(tid * run, last + 1), b1 = min(b0 + run, last + 1);
-  uint32_t over = 0, equal = 0;
-  for (int j = b0; j < b1; ++j) {
-    if (j == 0 || j == last || all) {
-      ++over;
-    } else if (want > 0) {
-      const uint64_t u = key[j] >> shift;
-      over += u > cut;
-      equal += u == cut;
+  s.sync();
+  const int cut = s.cut;
+  const uint32_t need = s.need, found = s.found;
+  const bool few = found <= s.kTied;
+  for (int j = 1 + tid; j < last; j += T) {
+    const double x = key[j];
+    const int b = bucket(x);
+    if (b > cut || (b == cut && found == need)) {
+      atomicOr(&s.kept[j / 32], 1u << (j % 32));
+    } else if (b == cut && few) {
+      const uint32_t n = atomicAdd(&s.tied, 1u);
+      s.tied_key[n] = x;
+      s.tied_at[n] = static_cast<uint16_t>(j);
     }
   }
-  const uint32_t before = block_scan(over << 16 | equal, wbuf);
-  uint32_t eq = before & 0xffffu;
-  uint32_t at = (before >> 16) + min(eq, ties);
-  for (int j = b0; j < b1; ++j) {
-    bool in = j == 0 || j == last || all;
-    if (!in && want > 0) {
-      const uint64_t u = key[j] >> shift;
-      in = u > cut;
-      if (u == cut) in = eq++ < ties;
+  s.sync();
+  if (found == need) return;
+  if (few) {
+    for (uint32_t i = tid; i < found; i += T) {
+      const double x = s.tied_key[i];
+      const int j = s.tied_at[i];
+      uint32_t rank = 0;
+      for (uint32_t n = 0; n < found; ++n) {
+        const double y = s.tied_key[n];
+        rank += y > x || (y == x && s.tied_at[n] < j);
+      }
+      if (rank < need) atomicOr(&s.kept[j / 32], 1u << (j % 32));
     }
-    if (in) {
-      if (at < static_cast<uint32_t>(r.kcap))
-        for (int h = 0; h < per; ++h) out[static_cast<int64_t>(h) * r.kcap + at] = j;
+    s.sync();
+    return;
+  }
+  // Many keys in one interval (equal blocks, or a few far outliers): their need-th largest value
+  // bit by bit, then the lowest blocks of those equal to it.
+  uint64_t t = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const uint64_t c = t | 1ull << bit;
+    uint32_t n = 0;
+    for (int j = 1 + tid; j < last; j += T) n += bucket(key[j]) == cut && rank_of(key[j]) >= c;
+    if (s.sum(n) >= need) t = c;
+  }
+  const int run = (last + T - 1) / T;
+  const int j0 = max(min(tid * run, last), 1), j1 = min(tid * run + run, last);
+  uint32_t above = 0, equal = 0;
+  for (int j = j0; j < j1; ++j) {
+    if (bucket(key[j]) != cut) continue;
+    const uint64_t u = rank_of(key[j]);
+    above += u > t;
+    equal += u == t;
+  }
+  const uint32_t ties = need - s.sum(above);
+  uint32_t at = s.prefix(equal);
+  for (int j = j0; j < j1; ++j) {
+    if (bucket(key[j]) != cut) continue;
+    const uint64_t u = rank_of(key[j]);
+    if (u > t || (u == t && at++ < ties)) atomicOr(&s.kept[j / 32], 1u << (j % 32));
+  }
+  s.sync();
+}
+
+// Writes the blocks of s.kept in ascending order as the lists of `per` heads, -1 behind them.
+template <int T, typename F>
+__device__ void write_list(Team<T>& s, int last, int kcap, int per, int32_t* idx, int32_t* cnt,
+                           F each) {
+  const int tid = s.tid(), halves = last < 0 ? 0 : (last / 32 + 1) * 2;
+  uint32_t total = 0;
+  for (int h0 = 0; h0 < halves; h0 += T) {  // thread t: 16 blocks
+    const int h = h0 + tid;
+    uint32_t bits = h < halves ? s.kept[h / 2] >> (16 * (h % 2)) & 0xffffu : 0u;
+    const uint32_t n = __popc(bits);
+    uint32_t at = total + s.prefix(n);
+    while (bits) {
+      const int j = h * 16 + __ffs(bits) - 1;
+      bits &= bits - 1;
+      if (at < static_cast<uint32_t>(kcap)) {
+        for (int p = 0; p < per; ++p) idx[static_cast<int64_t>(p) * kcap + at] = j;
+        each(at, j);
+      }
       ++at;
     }
+    total += s.sum(n);
   }
-  const int kept = min(want + min(last + 1, 2), r.kcap);
-  for (int n = kept + tid; n < r.kcap; n += kPickThreads)
-    for (int h = 0; h < per; ++h) out[static_cast<int64_t>(h) * r.kcap + n] = -1;
-  if (tid < per) r.sel_cnt[static_cast<int64_t>(row) * r.Hq + head + tid] = kept;
+  total = min(total, static_cast<uint32_t>(kcap));
+  for (int e = total + tid; e < kcap; e += T)
+    for (int p = 0; p < per; ++p) idx[static_cast<int64_t>(p) * kcap + e] = -1;
+  for (int p = tid; p < per; p += T) cnt[p] = static_cast<int32_t>(total);
+  s.sync();
+}
+
+union Teams {
+  Team<kThreads> cta;
+  Team<32> warp[kWarps];
+};
+
+struct Sums {
+  double lse[kHeads];               // softmax denominators of the pass's heads (ln)
+  double top[kMaxCluster][kHeads];  // each CTA's maximum and sum, in every CTA
+  double sum[kMaxCluster][kHeads];
+  uint32_t scan[kWarps];
+};
+
+struct Args {
+  KvCache c;
+  DecodeRows r;
+  const int32_t* budget;
+  SelMetric m;
+  DecodeLists lists;  // of the attention; list NULL: not wanted
+  int slice;          // blocks of a CTA
+};
+
+// Lists that a CTA of a cluster picks in a pass, with keys of their own.
+__host__ __device__ __forceinline__ int lists_of(bool group, int csize) {
+  return csize == 1 ? 0 : group ? 1 : (kHeads + csize - 1) / csize;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
+  constexpr int NI = D / 32;  // float4 of a lane and block
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ Sums s;
+  __shared__ Teams team;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int csize = gridDim.x, rank = blockIdx.x;  // (a cluster is a row of the grid)
+  const int row = blockIdx.z, kv = blockIdx.y, G = a.r.Hq / a.c.Hkv;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  // shared memory: queries (double) | scores of this CTA's blocks | their V terms | group sums |
+  // keys of the lists that this CTA picks (of a cluster of one: the scores' place) | (first CTA)
+  // head bits of each block
+  double* q_s = reinterpret_cast<double*>(smem);
+  double* score = q_s + kHeads * D;
+  double* w_s = score + kHeads * a.slice;
+  double* acc = w_s + a.slice;
+  double* key = csize == 1 ? score : acc + a.slice;
+  uint32_t* mask = reinterpret_cast<uint32_t*>(acc + a.slice +
+                                               lists_of(a.m.group, csize) * a.c.max_blocks);
+
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+  int seq, len;
+  decode_row(a.c, a.r, row, seq, len);
+  const int last = (len + a.c.block - 1) / a.c.block - 1;
+  int k = 0;
+  if (last >= 0) {
+    k = a.budget[last];
+    const int lo = min(last + 1, 2);
+    if (k < lo || k > last + 1 || k > a.r.kcap) {
+      if (a.r.status && tid == 0) *a.r.status = STEM_ERR_ARG;
+      k = min(max(k, lo), min(last + 1, a.r.kcap));
+    }
+  }
+  const int want = k - 2;                              // beside the sink and the diagonal block
+  const bool scored = want > 0 && want < last - 1;     // (else the scores decide nothing)
+  const bool product_group = a.m.group && !a.m.additive && G > 1;
+  const int j0 = min(rank * a.slice, max(last, 0)), j1 = min(j0 + a.slice, max(last, 0));
+  const int32_t* table = a.c.table + static_cast<int64_t>(seq) * a.c.max_blocks;
+  const double scale = 1.0 / sqrt(static_cast<double>(D));
+  const int key_row = csize == 1 ? a.slice : a.c.max_blocks;
+
+  if (scored) {
+    for (int j = j0 + tid; j < j1; j += kThreads) {
+      const int page = kv_page(a.c, seq, j, a.r.status);
+      w_s[j - j0] =
+          page < 0 ? NAN : magnitude(a.m, a.c.vnorm[static_cast<int64_t>(page) * a.c.Hkv + kv]);
+      acc[j - j0] = a.m.additive || G == 1 ? 0.0 : -INFINITY;
+    }
+  }
+  for (int h0 = 0; h0 < G; h0 += kHeads) {
+    const int nh = min(kHeads, G - h0);
+    const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
+    if (scored) {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.r.q) + head0 * D;
+      for (int n = tid; n < kHeads * D; n += kThreads)
+        q_s[n] = n < nh * D ? static_cast<double>(__bfloat162float(q[n])) * scale : 0.0;
+      __syncthreads();
+      // ---- scores: 8 lanes hold two blocks; lane l has channels 4l .. 4l + 3 of each 32
+      const int sub = lane / 8, l = lane % 8;
+      for (int b = j0 + warp * 8; b < j1; b += kWarps * 8) {
+        float4 x[2][NI];
+        bool there[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int j = b + sub * 2 + y;
+          const int page = j < j1 ? table[j] : -1;
+          const bool ok = there[y] = page >= 0 && page < a.c.num_pages;
+          const float4* p = reinterpret_cast<const float4*>(
+              a.c.kbar + (static_cast<int64_t>(ok ? page : 0) * a.c.Hkv + kv) * D);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) x[y][i] = ok ? p[i * 8 + l] : make_float4(0, 0, 0, 0);
+        }
+#pragma unroll 1
+        for (int g0 = 0; g0 < nh; g0 += 4) {
+          double v[4][2];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) v[h][0] = v[h][1] = 0.0;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            double k0[4] = {x[0][i].x, x[0][i].y, x[0][i].z, x[0][i].w};
+            double k1[4] = {x[1][i].x, x[1][i].y, x[1][i].z, x[1][i].w};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const double2* qp =
+                  reinterpret_cast<const double2*>(q_s + (g0 + h) * D + i * 32 + l * 4);
+              const double2 qa = qp[0], qb = qp[1];
+              v[h][0] = fma(qa.x, k0[0], v[h][0]);
+              v[h][1] = fma(qa.x, k1[0], v[h][1]);
+              v[h][0] = fma(qa.y, k0[1], v[h][0]);
+              v[h][1] = fma(qa.y, k1[1], v[h][1]);
+              v[h][0] = fma(qb.x, k0[2], v[h][0]);
+              v[h][1] = fma(qb.x, k1[2], v[h][1]);
+              v[h][0] = fma(qb.y, k0[3], v[h][0]);
+              v[h][1] = fma(qb.y, k1[3], v[h][1]);
+            }
+          }
+          // fold over the 8 lanes: lane bit 0 takes a block, bits 1 and 2 a head
+          double u[4], t[2], r;
+          const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            u[h] = (b0 ? v[h][1] : v[h][0]) + __shfl_xor_sync(kFull, b0 ? v[h][0] : v[h][1], 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            t[h] = (b1 ? u[h + 2] : u[h]) + __shfl_xor_sync(kFull, b1 ? u[h] : u[h + 2], 2);
+          r = (b2 ? t[1] : t[0]) + __shfl_xor_sync(kFull, b2 ? t[0] : t[1], 4);
+          const int h = g0 + (b1 ? 2 : 0) + (b2 ? 1 : 0), j = b + sub * 2 + (b0 ? 1 : 0);
+          if (j < j1) score[h * a.slice + j - j0] = there[b0 ? 1 : 0] ? r : -INFINITY;
+        }
+      }
+      __syncthreads();
+      if (product_group) {
+        // ---- each head's softmax denominator: a warp per head, then over the cluster
+        for (int h = warp; h < nh; h += kWarps) {
+          const double* sh = score + h * a.slice;
+          double top = -INFINITY, sum = 0.0;
+          for (int n = lane; n < j1 - j0; n += 32) top = fmax(top, sh[n]);
+          for (int o = 16; o; o /= 2) top = fmax(top, __shfl_xor_sync(kFull, top, o));
+          const double base = top > -INFINITY ? top : 0.0;
+          for (int n = lane; n < j1 - j0; n += 32) sum += exp(sh[n] - base);
+          for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(kFull, sum, o);
+          if (lane < csize) {
+            Sums* to = cluster.map_shared_rank(&s, lane);
+            to->top[rank][h] = top;
+            to->sum[rank][h] = sum;
+          }
+        }
+        cluster.sync();
+        if (tid < nh) {
+          double top = -INFINITY, sum = 0.0;
+          for (int c = 0; c < csize; ++c) top = fmax(top, s.top[c][tid]);
+          if (!(top > -INFINITY)) top = 0.0;
+          for (int c = 0; c < csize; ++c) {
+            const double base = s.top[c][tid] > -INFINITY ? s.top[c][tid] : 0.0;
+            sum += s.sum[c][tid] * exp(base - top);
+          }
+          s.lse[tid] = top + log(sum);
+        }
+        __syncthreads();
+      }
+      // ---- keys, or the group's sum so far
+      if (a.m.group) {
+        for (int n = tid; n < j1 - j0; n += kThreads) {
+          double x = acc[n];
+          if (product_group) {
+            // ln of the probabilities' sum; relative to the largest where the plain sum would lose
+            // digits to the range's end (and after the first 8 heads)
+            double sum = 0.0;
+            if (h0 == 0)
+              for (int h = 0; h < nh; ++h) sum += exp(score[h * a.slice + n] - s.lse[h]);
+            if (sum > 1e-280 || isnan(sum)) {
+              x = log(sum);
+            } else {
+              double top = x;
+              for (int h = 0; h < nh; ++h) top = fmax(top, score[h * a.slice + n] - s.lse[h]);
+              if (top > -INFINITY) {
+                sum = exp(x - top);
+                for (int h = 0; h < nh; ++h) sum += exp(score[h * a.slice + n] - s.lse[h] - top);
+                x = top + log(sum);
+              }
+            }
+          } else {
+            for (int h = 0; h < nh; ++h) x += score[h * a.slice + n];
+          }
+          acc[n] = x;
+          // (in a cluster of one the key takes the place of the block's first score)
+          if (h0 + nh == G)
+            *cluster.map_shared_rank(key + j0 + n, 0) =
+                as_key(x + (a.m.additive ? G * w_s[n] : w_s[n]));
+        }
+      } else {
+        for (int n = tid; n < nh * a.slice; n += kThreads) {
+          const int h = n / a.slice, e = n % a.slice;
+          if (e >= j1 - j0) continue;
+          *cluster.map_shared_rank(key + (h / csize) * key_row + j0 + e, h % csize) =
+              as_key(score[n] + w_s[e]);
+        }
+      }
+    }
+    if (a.m.group && h0 + nh < G) {
+      cluster.sync();  // (the next heads' sums go where these were read)
+      continue;
+    }
+    if (!a.m.group && rank == 0 && a.lists.list)
+      for (int w = tid; w < last / 4 + 1; w += kThreads) mask[w] = 0;
+    if (scored || !a.m.group) cluster.sync();
+    // ---- pick
+    if (a.m.group) {  // one list for all heads: the first CTA's
+      if (rank == 0) {
+        Team<kThreads>& tm = team.cta;
+        if (last >= 0) pick(key, last, want, tm);
+        const int64_t li = static_cast<int64_t>(row) * a.c.Hkv + kv;
+        Entry* list = a.lists.list ? a.lists.list + li * a.lists.most : nullptr;
+        const int64_t head = static_cast<int64_t>(row) * a.r.Hq + kv * G;
+        write_list(tm, last, a.r.kcap, G, a.r.sel_idx + head * a.r.kcap, a.r.sel_cnt + head,
+                   [&](uint32_t at, int j) {
+                     if (list) list[at] = entry_of(a.c, seq, j, 0xffu, a.r.status);
+                   });
+        if (list && tid == 0) a.lists.count[li] = max(min(k, a.r.kcap), 0);
+      }
+      continue;
+    }
+    // a list a head: spread over the cluster, and with four or more in a CTA over its warps
+    uint32_t* mask0 = cluster.map_shared_rank(mask, 0);
+    auto head_list = [&](auto& tm, int h) {
+      if (last >= 0) pick(key + (h / csize) * key_row, last, want, tm);
+      write_list(tm, last, a.r.kcap, 1, a.r.sel_idx + (head0 + h) * a.r.kcap,
+                 a.r.sel_cnt + head0 + h, [&](uint32_t, int j) {
+                   if (a.lists.list) atomicOr(&mask0[j / 4], 1u << (8 * (j % 4) + h));
+                 });
+    };
+    if (csize <= 2) {
+      const int h = rank + warp * csize;
+      if (h < nh) head_list(team.warp[warp], h);
+    } else {
+      for (int h = rank; h < nh; h += csize) head_list(team.cta, h);
+    }
+    cluster.sync();
+    if (rank == 0 && a.lists.list) {
+      const int64_t item = (static_cast<int64_t>(row) * a.c.Hkv + kv) * a.lists.tiles_h + h0 / kHeads;
+      write_union<kThreads>(a.c, a.lists, item, seq, last, nh, mask, s.scan, a.r.status);
+    }
+    __syncthreads();
+  }
+  cluster.sync();  // (no CTA leaves while another may still write to it)
 }
 
 }  // namespace
 
 cudaError_t launch_decode_select(const KvCache& c, int D, const DecodeRows& r,
-                                 const int32_t* budget, SelMetric metric, double* scores,
+                                 const int32_t* budget, SelMetric metric, const DecodeLists& lists,
                                  cudaStream_t st) {
-  const dim3 grid((c.max_blocks + kScoreBlocks - 1) / kScoreBlocks, c.Hkv, r.R);
-  if (D == 128)
-    score_kernel<128><<<grid, kScoreWarps * 32, 0, st>>>(c, r, scores);
-  else
-    score_kernel<64><<<grid, kScoreWarps * 32, 0, st>>>(c, r, scores);
-  cudaError_t e = cudaGetLastError();
+  // Clusters grow while the device has room for more CTAs and a CTA has blocks to share.
+  const int64_t lists_all = static_cast<int64_t>(r.R) * c.Hkv;
+  int csize = 1;
+  while (csize < kMaxCluster &&
+         (c.max_blocks > csize * kMaxSlice ||
+          (lists_all * csize < 2 * sm_count() && c.max_blocks > csize * kSlice)))
+    csize *= 2;
+  const Args a{c, r, budget, metric, lists, (c.max_blocks + csize - 1) / csize};
+  const size_t bytes = sizeof(double) * (static_cast<size_t>(kHeads) * (D + a.slice) + 2 * a.slice +
+                                         static_cast<size_t>(lists_of(metric.group, csize)) *
+                                             c.max_blocks) +
+                       (static_cast<size_t>(c.max_blocks) + 7) / 4 * 4;
+  void (*kernel)(const Args) = D == 128 ? select_kernel<128> : select_kernel<64>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  const dim3 pgrid(metric.group ? c.Hkv : r.Hq, r.R);
-  pick_kernel<<<pgrid, kPickThreads, c.max_blocks * sizeof(uint64_t), st>>>(c, r, budget, metric,
-                                                                            scores);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(csize, c.Hkv, r.R), kThreads, bytes, csize, st, a);
 }
 
 }  // namespace stem
