@@ -10,9 +10,9 @@
 // this costs less than reading kbar: 2 G D flops a block and kv head against 4 D bytes.
 //
 // One cluster of up to 8 CTAs per (row, kv head), so that scores never leave shared memory and a
-// single launch does it all: each CTA scores a run of blocks for 8 heads at a time (a lane holds 16
-// channels of two blocks and meets them with one head after the other), the heads' softmax sums and
-// then the keys are exchanged through distributed shared memory, and each list is picked by one
+// single launch does it all: each CTA scores a run of blocks for 8 heads at a time on the
+// double-precision MMA (its operands need no shared memory and no reduction between lanes, which
+// bound the form with plain FMAs), the heads' softmax sums and then the keys are exchanged through distributed shared memory, and each list is picked by one
 // CTA of the cluster. Latency bounds it for a few rows, reading kbar for many.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -263,6 +263,15 @@ struct Sums {
   uint32_t scan[kWarps];
 };
 
+// D += A B with A 16 x 4 (rows g and g + 8), B 4 x 8.
+__device__ __forceinline__ void mma_f64(double (&d)[4], double a0, double a1, double b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k4.row.col.f64.f64.f64.f64 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+      "{%0,%1,%2,%3};"
+      : "+d"(d[0]), "+d"(d[1]), "+d"(d[2]), "+d"(d[3])
+      : "d"(a0), "d"(a1), "d"(b));
+}
+
 struct Args {
   KvCache c;
   DecodeRows r;
@@ -287,11 +296,10 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
   const int csize = gridDim.x, rank = blockIdx.x;  // (a cluster is a row of the grid)
   const int row = blockIdx.z, kv = blockIdx.y, G = a.r.Hq / a.c.Hkv;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  // shared memory: queries (double) | scores of this CTA's blocks | their V terms | group sums |
+  // shared memory: scores of this CTA's blocks | their V terms | group sums |
   // keys of the lists that this CTA picks (of a cluster of one: the scores' place) | (first CTA)
   // head bits of each block
-  double* q_s = reinterpret_cast<double*>(smem);
-  double* score = q_s + kHeads * D;
+  double* score = reinterpret_cast<double*>(smem);
   double* w_s = score + kHeads * a.slice;
   double* acc = w_s + a.slice;
   double* key = csize == 1 ? score : acc + a.slice;
@@ -332,61 +340,54 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
     const int nh = min(kHeads, G - h0);
     const int64_t head0 = static_cast<int64_t>(row) * a.r.Hq + kv * G + h0;
     if (scored) {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.r.q) + head0 * D;
-      for (int n = tid; n < kHeads * D; n += kThreads)
-        q_s[n] = n < nh * D ? static_cast<double>(__bfloat162float(q[n])) * scale : 0.0;
-      __syncthreads();
-      // ---- scores: 8 lanes hold two blocks; lane l has channels 4l .. 4l + 3 of each 32
-      const int sub = lane / 8, l = lane % 8;
-      for (int b = j0 + warp * 8; b < j1; b += kWarps * 8) {
-        float4 x[2][NI];
+      // ---- scores on the double-precision MMA: rows are blocks, columns heads. Lane 4g + t holds
+      // block g's (and g + 8's) and head g's channels 16i + 4t + e, which are column t of step (i, e).
+      const int g = lane / 4, t = lane % 4;
+      double q[D / 16][4];
+      const uint2* qp = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.r.q) +
+                                                       (head0 + (g < nh ? g : 0)) * D + 4 * t);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint2 u = g < nh ? qp[i * 4] : make_uint2(0, 0);
+        q[i][0] = static_cast<double>(__uint_as_float(u.x << 16)) * scale;
+        q[i][1] = static_cast<double>(__uint_as_float(u.x & 0xffff0000u)) * scale;
+        q[i][2] = static_cast<double>(__uint_as_float(u.y << 16)) * scale;
+        q[i][3] = static_cast<double>(__uint_as_float(u.y & 0xffff0000u)) * scale;
+      }
+      for (int b = j0 + warp * 16; b < j1; b += kWarps * 16) {
+        const float4* p[2];
         bool there[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const int j = b + sub * 2 + y;
+          const int j = b + g + 8 * y;
           const int page = j < j1 ? table[j] : -1;
-          const bool ok = there[y] = page >= 0 && page < a.c.num_pages;
-          const float4* p = reinterpret_cast<const float4*>(
-              a.c.kbar + (static_cast<int64_t>(ok ? page : 0) * a.c.Hkv + kv) * D);
-#pragma unroll
-          for (int i = 0; i < NI; ++i) x[y][i] = ok ? p[i * 8 + l] : make_float4(0, 0, 0, 0);
+          there[y] = page >= 0 && page < a.c.num_pages;
+          p[y] = reinterpret_cast<const float4*>(
+              a.c.kbar + (static_cast<int64_t>(there[y] ? page : 0) * a.c.Hkv + kv) * D + 4 * t);
         }
-#pragma unroll 1
-        for (int g0 = 0; g0 < nh; g0 += 4) {
-          double v[4][2];
+        double v[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-          for (int h = 0; h < 4; ++h) v[h][0] = v[h][1] = 0.0;
+        for (int i0 = 0; i0 < D / 16; i0 += 4) {
+          float4 x[4][2];
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            double k0[4] = {x[0][i].x, x[0][i].y, x[0][i].z, x[0][i].w};
-            double k1[4] = {x[1][i].x, x[1][i].y, x[1][i].z, x[1][i].w};
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const double2* qp =
-                  reinterpret_cast<const double2*>(q_s + (g0 + h) * D + i * 32 + l * 4);
-              const double2 qa = qp[0], qb = qp[1];
-              v[h][0] = fma(qa.x, k0[0], v[h][0]);
-              v[h][1] = fma(qa.x, k1[0], v[h][1]);
-              v[h][0] = fma(qa.y, k0[1], v[h][0]);
-              v[h][1] = fma(qa.y, k1[1], v[h][1]);
-              v[h][0] = fma(qb.x, k0[2], v[h][0]);
-              v[h][1] = fma(qb.x, k1[2], v[h][1]);
-              v[h][0] = fma(qb.y, k0[3], v[h][0]);
-              v[h][1] = fma(qb.y, k1[3], v[h][1]);
-            }
+            for (int y = 0; y < 2; ++y)
+              x[i][y] = there[y] ? p[y][(i0 + i) * 4] : make_float4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mma_f64(v, x[i][0].x, x[i][1].x, q[i0 + i][0]);
+            mma_f64(v, x[i][0].y, x[i][1].y, q[i0 + i][1]);
+            mma_f64(v, x[i][0].z, x[i][1].z, q[i0 + i][2]);
+            mma_f64(v, x[i][0].w, x[i][1].w, q[i0 + i][3]);
           }
-          // fold over the 8 lanes: lane bit 0 takes a block, bits 1 and 2 a head
-          double u[4], t[2], r;
-          const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+        }
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
-            u[h] = (b0 ? v[h][1] : v[h][0]) + __shfl_xor_sync(kFull, b0 ? v[h][0] : v[h][1], 1);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            t[h] = (b1 ? u[h + 2] : u[h]) + __shfl_xor_sync(kFull, b1 ? u[h] : u[h + 2], 2);
-          r = (b2 ? t[1] : t[0]) + __shfl_xor_sync(kFull, b2 ? t[0] : t[1], 4);
-          const int h = g0 + (b1 ? 2 : 0) + (b2 ? 1 : 0), j = b + sub * 2 + (b0 ? 1 : 0);
-          if (j < j1) score[h * a.slice + j - j0] = there[b0 ? 1 : 0] ? r : -INFINITY;
+        for (int y = 0; y < 2; ++y) {
+          const int j = b + g + 8 * y;
+          if (j >= j1) continue;
+          score[2 * t * a.slice + j - j0] = there[y] ? v[2 * y] : -INFINITY;
+          score[(2 * t + 1) * a.slice + j - j0] = there[y] ? v[2 * y + 1] : -INFINITY;
         }
       }
       __syncthreads();
@@ -519,7 +520,7 @@ cudaError_t launch_decode_select(const KvCache& c, int D, const DecodeRows& r,
           (lists_all * csize < 2 * sm_count() && c.max_blocks > csize * kSlice)))
     csize *= 2;
   const Args a{c, r, budget, metric, lists, (c.max_blocks + csize - 1) / csize};
-  const size_t bytes = sizeof(double) * (static_cast<size_t>(kHeads) * (D + a.slice) + 2 * a.slice +
+  const size_t bytes = sizeof(double) * (static_cast<size_t>(kHeads + 2) * a.slice +
                                          static_cast<size_t>(lists_of(metric.group, csize)) *
                                              c.max_blocks) +
                        (static_cast<size_t>(c.max_blocks) + 7) / 4 * 4;
