@@ -517,7 +517,7 @@ cudaError_t launch_decode_select(const KvCache& c, int D, const DecodeRows& r,
   int csize = 1;
   while (csize < kMaxCluster &&
          (c.max_blocks > csize * kMaxSlice ||
-          (lists_all * csize < 2 * sm_count() && c.max_blocks > csize * kSlice)))
+          (lists_all * csize < sm_count() && c.max_blocks > csize * kSlice)))
     csize *= 2;
   const Args a{c, r, budget, metric, lists, (c.max_blocks + csize - 1) / csize};
   const size_t bytes = sizeof(double) * (static_cast<size_t>(kHeads + 2) * a.slice +
