@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include "decode_internal.h"
+#include "decode_launch.h"
 #include "kv_layout.cuh"
 
 namespace stem {
@@ -271,6 +272,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache c, Rows r, con
   constexpr int CH = D / 8;                    // chunks of a row
   constexpr int SLOTS = kThreads / (8 * CH);  // tiles at a time
   int page, first, lo, hi;
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
   if (!my_block(c, r, page, first, lo, hi)) return;
   const int head = blockIdx.y, slot = threadIdx.x / (8 * CH);
   const int pair = threadIdx.x / CH % 8, chunk = threadIdx.x % CH;
@@ -437,6 +440,8 @@ __global__ void __launch_bounds__(8 * (D / 8)) read_kernel(KvCache c, Rows r, T*
   constexpr int CH = D / 8;
   int page, first, lo, hi;
   const int parts = c.block / (kReadTiles * kKvTile);
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
   if (!my_block(c, r, page, first, lo, hi, parts)) return;
   const int head = blockIdx.y, pair = threadIdx.x / CH, chunk = threadIdx.x % CH;
   const Place<FMT, D> at(pair, chunk);
@@ -468,13 +473,10 @@ cudaError_t launch(bool write, const KvCache& c, const Rows& r, void* k, void* v
   const unsigned nblk = static_cast<unsigned>((r.T + c.block - 2) / c.block + 1);
   const unsigned parts = write ? 1 : c.block / (kReadTiles * kKvTile);
   const dim3 grid(nblk * parts, c.Hkv, c.nseq);
-  if (write)
-    append_kernel<FMT, D, T><<<grid, kThreads, 0, st>>>(c, r, static_cast<const T*>(k),
-                                                        static_cast<const T*>(v));
-  else
-    read_kernel<FMT, D, T><<<grid, 8 * (D / 8), 0, st>>>(c, r, static_cast<T*>(k),
-                                                         static_cast<T*>(v));
-  return cudaGetLastError();
+  return write ? launch_after(append_kernel<FMT, D, T>, grid, kThreads, 0, 1, st, c, r,
+                              static_cast<const T*>(k), static_cast<const T*>(v))
+               : launch_after(read_kernel<FMT, D, T>, grid, 8 * (D / 8), 0, 1, st, c, r,
+                              static_cast<T*>(k), static_cast<T*>(v));
 }
 
 template <int FMT, int D>

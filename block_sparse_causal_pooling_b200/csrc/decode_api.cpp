@@ -143,6 +143,7 @@ int check_decode(const stem_decode_args_t* a, bool select, bool attend) {
     return STEM_ERR_ARG;
   if (select && (!a->budget || !aligned(a->budget, 4))) return STEM_ERR_ARG;
   if (attend && (!a->out || !aligned(a->out, 16) || !aligned(a->lse, 4))) return STEM_ERR_ARG;
+  if (!attend) return STEM_OK;  // (the selection keeps everything on chip)
   if (a->workspace == nullptr || !aligned(a->workspace, kAlign) ||
       a->workspace_bytes < workspace(a->cache, a->R, a->Hq, a->kcap))
     return STEM_ERR_WORKSPACE;

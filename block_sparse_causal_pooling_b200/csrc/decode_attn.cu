@@ -904,7 +904,7 @@ cudaError_t launch(const Args& a, bool planned, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   constexpr size_t bytes = static_cast<size_t>(kWarps) * C::RING;
-  // the attribute is per device; setting it is cheap and idempotent
+  // (per device and context; 0.1 us)
   e = cudaFuncSetAttribute(attn_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes));
   if (e != cudaSuccess) return e;

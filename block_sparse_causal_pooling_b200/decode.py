@@ -15,6 +15,7 @@ passes its own outputs and workspace too, or orders the two streams itself.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -28,6 +29,7 @@ _lib = _stem.lib()
 _FORMATS = {"bf16": STEM_KV_BF16, "q8": STEM_KV_Q8, "q4": STEM_KV_Q4}
 _VSUMS = {"mean": STEM_VSUM_MEAN, "max": STEM_VSUM_MAX}
 _SHARES = {"head": STEM_SHARE_HEAD, "group": STEM_SHARE_GROUP}
+_ATTN = {k: stem_method_t(share=v) for k, v in _SHARES.items()}  # all that the attention reads
 _Strides = ctypes.c_int64 * 3
 
 __all__ = ["PagedCache", "stem_cache_page_bytes", "stem_cache_append", "stem_cache_read",
@@ -36,16 +38,18 @@ __all__ = ["PagedCache", "stem_cache_page_bytes", "stem_cache_append", "stem_cac
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device) -> None:
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
+@functools.lru_cache(maxsize=None)
 def stem_cache_page_bytes(D: int, block: int, fmt: str) -> int:
     """Bytes of the record of one (page, kv head); 0 if the library does not support the shape."""
     return int(_lib.stem_cache_page_bytes(D, block, _FORMATS[fmt]))
@@ -60,7 +64,7 @@ class PagedCache:
     """
 
     __slots__ = ("pages", "kbar", "vnorm", "table", "block", "fmt", "vsum", "device", "D", "Hkv",
-                 "nseq", "max_blocks", "c", "ref")
+                 "nseq", "max_blocks", "c", "at")
 
     def __init__(self, pages, kbar, vnorm, table, block: int, fmt: str, vsum: str = "mean"):
         if kbar.dim() != 3 or table.dim() != 2:
@@ -71,7 +75,7 @@ class PagedCache:
             raise ValueError(f"vsum must be one of {sorted(_VSUMS)}, got {vsum!r}")
         n, Hkv, D = kbar.shape
         dev = pages.device
-        size = _lib.stem_cache_page_bytes(D, block, _FORMATS[fmt])
+        size = stem_cache_page_bytes(D, block, fmt)
         if size == 0:
             raise ValueError(f"D and block must be 64 or 128, got {D} and {block}")
         if dev.type != "cuda":
@@ -80,14 +84,14 @@ class PagedCache:
         _need(kbar, "kbar", torch.float32, (n, Hkv, D), dev)
         _need(vnorm, "vnorm", torch.float32, (n, Hkv), dev)
         _need(table, "table", torch.int32, table.shape, dev)
+        nseq, max_blocks = table.shape
         self.pages, self.kbar, self.vnorm, self.table = pages, kbar, vnorm, table
         self.block, self.fmt, self.vsum, self.device = block, fmt, vsum, dev
-        self.D, self.Hkv = D, Hkv
-        self.nseq, self.max_blocks = table.shape
+        self.D, self.Hkv, self.nseq, self.max_blocks = D, Hkv, nseq, max_blocks
         self.c = stem_cache_t(pages.data_ptr(), kbar.data_ptr(), vnorm.data_ptr(),
-                              table.data_ptr(), n, Hkv, D, block, _FORMATS[fmt], self.nseq,
-                              self.max_blocks, _VSUMS[vsum])
-        self.ref = ctypes.byref(self.c)
+                              table.data_ptr(), n, Hkv, D, block, _FORMATS[fmt], nseq, max_blocks,
+                              _VSUMS[vsum])
+        self.at = ctypes.addressof(self.c)
 
     @classmethod
     def alloc(cls, num_pages: int, Hkv: int, D: int, block: int, fmt: str, table: torch.Tensor,
@@ -107,14 +111,16 @@ def _launch(fn, cache: PagedCache, stream, *args):
     """fn(*args, stream) with the cache's device current."""
     dev = cache.device
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
     elif stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the cache on {dev}")
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, stream.cuda_stream)
+    else:
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(*args, stream)
     if rc:
         raise StemError(rc, fn.__name__)
 
@@ -152,7 +158,7 @@ def _rows(fn, cache, k, v, pos, count, status, stream):
     _need(pos, "pos", torch.int32, (cache.nseq,), dev)
     if count is not None:
         _need(count, "count", torch.int32, (cache.nseq,), dev)
-    _launch(fn, cache, stream, cache.ref, k.data_ptr(), v.data_ptr(), code, T,
+    _launch(fn, cache, stream, cache.at, k.data_ptr(), v.data_ptr(), code, T,
             _Strides(*strides[:3]), pos.data_ptr(), None if count is None else count.data_ptr(),
             _status(status, dev))
 
@@ -193,7 +199,15 @@ def stem_decode_budget(max_blocks: int, method: stem_method_t, device):
 
 def stem_decode_workspace_size(cache: PagedCache, R: int, Hq: int, kcap: int) -> int:
     """Workspace bytes of a decode call of R rows; one workspace per call that may overlap another."""
-    return int(_lib.stem_decode_workspace_size(cache.ref, R, Hq, kcap))
+    return _workspace_size(cache.device.index, cache.fmt, cache.D, cache.block, cache.Hkv,
+                           cache.max_blocks, R, Hq, kcap)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(device, fmt, D, block, Hkv, max_blocks, R, Hq, kcap):
+    c = stem_cache_t(None, None, None, None, 1, Hkv, D, block, _FORMATS[fmt], 1, max_blocks, 0)
+    with torch.cuda.device(device):
+        return int(_lib.stem_decode_workspace_size(ctypes.addressof(c), R, Hq, kcap))
 
 
 def _decode(fn, cache, q, lens, rows, budget, kcap, method, sel_idx, sel_cnt, out, lse, workspace,
@@ -201,33 +215,36 @@ def _decode(fn, cache, q, lens, rows, budget, kcap, method, sel_idx, sel_cnt, ou
     dev = cache.device
     if q.dim() != 3 or q.shape[2] != cache.D:
         raise ValueError(f"q must be [R, Hq, {cache.D}], got {tuple(q.shape)}")
-    R, Hq, D = q.shape
-    _need(q, "q", torch.bfloat16, q.shape, dev)
+    R, Hq, D = shape = q.shape
+    _need(q, "q", torch.bfloat16, shape, dev)
     _need(lens, "lens", torch.int32, (R,), dev)
     if rows is not None:
         _need(rows, "rows", torch.int32, (R,), dev)
+        rows = rows.data_ptr()
     if budget is not None:
         _need(budget, "budget", torch.int32, (cache.max_blocks,), dev)
+        budget = budget.data_ptr()
     _need(sel_idx, "sel_idx", torch.int32, (R, Hq, kcap), dev)
     _need(sel_cnt, "sel_cnt", torch.int32, (R, Hq), dev)
-    if out is not None:
-        _need(out, "out", torch.bfloat16, q.shape, dev)
+    if out is None:  # a selection alone needs no workspace
+        at, size, out = None, 0, None
+    else:
+        _need(out, "out", torch.bfloat16, shape, dev)
+        out = out.data_ptr()
+        if workspace is None:
+            workspace = torch.empty(stem_decode_workspace_size(cache, R, Hq, kcap),
+                                    dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or workspace.dtype is not torch.uint8 or \
+                not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+        at, size = workspace.data_ptr(), workspace.numel()
     if lse is not None:
         _need(lse, "lse", torch.float32, (R, Hq), dev)
-    if workspace is None:
-        workspace = torch.empty(max(_lib.stem_decode_workspace_size(cache.ref, R, Hq, kcap), 256),
-                                dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or workspace.dtype is not torch.uint8 or \
-            not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
-    a = stem_decode_args_t(ctypes.pointer(cache.c), q.data_ptr(),
-                           None if rows is None else rows.data_ptr(), lens.data_ptr(),
-                           None if budget is None else budget.data_ptr(), R, Hq, kcap, STEM_BF16,
-                           ctypes.pointer(method), sel_idx.data_ptr(), sel_cnt.data_ptr(),
-                           None if out is None else out.data_ptr(),
-                           None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                           workspace.numel(), _status(status, dev))
-    _launch(fn, cache, stream, ctypes.byref(a))
+        lse = lse.data_ptr()
+    a = stem_decode_args_t(cache.at, q.data_ptr(), rows, lens.data_ptr(), budget, R, Hq, kcap,
+                           STEM_BF16, ctypes.addressof(method), sel_idx.data_ptr(),
+                           sel_cnt.data_ptr(), out, lse, at, size, _status(status, dev))
+    _launch(fn, cache, stream, ctypes.addressof(a))
 
 
 def _lists(q, kcap, sel_idx, sel_cnt):
@@ -241,14 +258,13 @@ def _lists(q, kcap, sel_idx, sel_cnt):
 
 
 def stem_decode_select(cache: PagedCache, q, lens, budget, kcap: int, method: stem_method_t,
-                       rows=None, sel_idx=None, sel_cnt=None, workspace=None, status=None,
-                       stream=None):
+                       rows=None, sel_idx=None, sel_cnt=None, status=None, stream=None):
     """Kept blocks of query tokens q [R, Hq, D] (bf16) that see lens[r] tokens of sequence rows[r]
     (None: sequence r). Returns (sel_idx [R, Hq, kcap], ascending, -1 past the count, and sel_cnt
     [R, Hq])."""
     sel_idx, sel_cnt = _lists(q, kcap, sel_idx, sel_cnt)
     _decode(_lib.stem_decode_select, cache, q, lens, rows, budget, kcap, method, sel_idx, sel_cnt,
-            None, None, workspace, status, stream)
+            None, None, None, status, stream)
     return sel_idx, sel_cnt
 
 
@@ -265,9 +281,8 @@ def stem_decode_attn(cache: PagedCache, q, lens, sel_idx, sel_cnt, share: str = 
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    m = stem_method_t(share=_SHARES[share])
-    _decode(_lib.stem_decode_attn, cache, q, lens, rows, None, sel_idx.shape[2], m, sel_idx,
-            sel_cnt, out, lse, workspace, status, stream)
+    _decode(_lib.stem_decode_attn, cache, q, lens, rows, None, sel_idx.shape[2], _ATTN[share],
+            sel_idx, sel_cnt, out, lse, workspace, status, stream)
     return out, lse
 
 
