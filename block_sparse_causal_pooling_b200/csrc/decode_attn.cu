@@ -136,10 +136,7 @@ struct Args {
   bool share;
   DecodeLists lists;
   int items;  // R * Hkv * lists.tiles_h: a row, a kv head and up to 8 of its query heads
-  // Entry numbers run over the items in order; CTA n of N = min(ctas, total) takes total * n / N and
-  // up (at least one).
   int ctas;
-  int64_t* start;  // [items]: number of the item's first entry; [items]: total
   __nv_bfloat16* out;
   float* lse;
   // [2 * ctas][8] statistics (max in log2 units, sum for the output, sum for lse) and [D] numerators
@@ -162,6 +159,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
   Entry* out = a.lists.list + list * a.lists.most;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
+  const int here = a.share ? a.lists.tiles_h : 1;  // items of this list
+  for (int n = tid; n < here; n += kPlanThreads) a.lists.arrived[list * here + n] = 0;
   int seq, len;
   decode_row(a.c, a.r, row, seq, len);
   const int last = (len + a.c.block - 1) / a.c.block - 1;
@@ -213,44 +212,114 @@ __device__ __forceinline__ int list_of(const Args& a, int item) {
   return a.share ? item / a.lists.tiles_h : item;
 }
 
-// Where a CTA starts: the total number of entries, and the item and the entry in it that its first
-// entry is. The CTA sums the counts of all items (every CTA the same ones, from L2).
-struct Begin {
-  int64_t total;
-  int item, entry;
-  int64_t start;  // number of the item's first entry
+// Entries are numbered over the items in order and spread evenly over N = min(ctas, total) CTAs: the
+// first total % N of them take one more than the others.
+struct Spread {
+  int total, each, more;
+  __device__ __forceinline__ Spread(int total_, int ctas) : total(total_) {
+    const int n = max(min(ctas, total), 1);
+    each = total / n;
+    more = total - each * n;
+  }
+  __device__ __forceinline__ int first(int cta) const {  // (total for the CTAs without entries)
+    return min(each * cta + min(cta, more), total);
+  }
+  __device__ __forceinline__ int cta_of(int entry) const {
+    const int b = more * (each + 1);
+    return entry < b ? entry / (each + 1) : more + (entry - b) / each;
+  }
 };
-__device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int64_t* wsum) {
+
+// The item that a CTA's first entry is in, and the entry's number there. The CTA sums the counts of
+// all items (every CTA the same ones, from L2).
+struct Begin {
+  int total, item, entry;
+};
+__device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int* wsum) {
   const int tid = threadIdx.x, run = (a.items + kWarps * 32 - 1) / (kWarps * 32);
   const int i0 = min(tid * run, a.items), i1 = min(i0 + run, a.items);
-  int64_t n = 0;
+  int n = 0;
   for (int i = i0; i < i1; ++i) n += a.lists.count[list_of(a, i)];
-  int64_t s = n;
+  int s = n;
   for (int o = 1; o < 32; o *= 2) {
-    const int64_t y = __shfl_up_sync(kFull, s, o);
+    const int y = __shfl_up_sync(kFull, s, o);
     if (tid % 32 >= o) s += y;
   }
   if (tid % 32 == 31) wsum[tid / 32] = s;
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
   for (int w = 0; w < kWarps; ++w) {
     if (w < tid / 32) s += wsum[w];
     total += wsum[w];
   }
   s -= n;
-  const int64_t first = total * blockIdx.x / max(min(static_cast<int64_t>(a.ctas), total), int64_t{1});
-  if (blockIdx.x < total && first >= s && first < s + n) {
+  const int first = Spread(total, a.ctas).first(blockIdx.x);
+  if (first >= s && first < s + n) {
     int i = i0;
     for (;; ++i) {
       const int c = a.lists.count[list_of(a, i)];
       if (first < s + c) break;
       s += c;
     }
-    *sh = Begin{total, i, static_cast<int>(first - s), s};
-  } else if (blockIdx.x >= total && tid == 0) {
-    *sh = Begin{total, 0, 0, 0};  // more CTAs than entries
+    *sh = Begin{total, i, first - s};
+  } else if (first >= total && tid == 0) {
+    *sh = Begin{total, 0, 0};  // no entries here
   }
   __syncthreads();
+}
+
+// Joins the parts of an item, once they are all there: a warp for each head, a lane for 4 channels
+// (at 64 channels the warp's halves take parts in turn). slot(s) is where part s is.
+template <int D, typename F>
+__device__ __forceinline__ void join_parts(const Args& a, int64_t head0, int nh, int parts, F slot) {
+  constexpr int kLanes = D / 4, kHalves = 32 / kLanes;
+  const int lane = threadIdx.x % 32, c = lane % kLanes, half = lane / kLanes;
+  for (int h = threadIdx.x / 32; h < nh; h += kWarps) {
+    float m = -INFINITY;
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, __ldcg(&a.stat[slot(s) * kHeadTile + h]).x);
+    for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, lx = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+      float f = 0.f;
+      if (s0 + lane < parts) {
+        const float4 st = __ldcg(&a.stat[slot(s0 + lane) * kHeadTile + h]);
+        f = exp2f(st.x - base);
+        l = fmaf(f, st.y, l);
+        lx = fmaf(f, st.z, lx);
+      }
+      const int n = min(parts - s0, 32);
+#pragma unroll 8
+      for (int i = 0; i < n; i += kHalves) {
+        const int e = i + half;
+        const float w = __shfl_sync(kFull, f, e & 31);
+        if (e < n) {
+          const float4 p = __ldcg(reinterpret_cast<const float4*>(
+                                      a.part + (static_cast<int64_t>(slot(s0 + e)) * kHeadTile + h) * D) + c);
+          x.x = fmaf(w, p.x, x.x);
+          x.y = fmaf(w, p.y, x.y);
+          x.z = fmaf(w, p.z, x.z);
+          x.w = fmaf(w, p.w, x.w);
+        }
+      }
+    }
+    for (int o = 16; o; o /= 2) {
+      l += __shfl_xor_sync(kFull, l, o);
+      lx += __shfl_xor_sync(kFull, lx, o);
+    }
+    if (kHalves == 2) {
+      x.x += __shfl_xor_sync(kFull, x.x, 16);
+      x.y += __shfl_xor_sync(kFull, x.y, 16);
+      x.z += __shfl_xor_sync(kFull, x.z, 16);
+      x.w += __shfl_xor_sync(kFull, x.w, 16);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (half == 0)
+      *reinterpret_cast<uint2*>(a.out + (head0 + h) * D + 4 * c) =
+          make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+    if (lane == 0 && a.lse) a.lse[head0 + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+  }
 }
 
 template <int FMT, int D>
@@ -261,7 +330,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
   constexpr int NG = L::NG, TPS = C::TPS;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Begin s_begin;
-  __shared__ int64_t s_sum[kWarps];
+  __shared__ int s_sum[kWarps];
+  __shared__ bool s_last;
   __shared__ Entry ent[kStaged];
   __shared__ float s_m[kWarps][kHeadTile], s_l[kWarps][kHeadTile], s_x[kWarps][kHeadTile];
 
@@ -270,22 +340,27 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
   find_begin(a, &s_begin, s_sum);
-  const int64_t total = s_begin.total;
-  if (blockIdx.x == 0 && tid == 0) a.start[a.items] = total;
-  const int64_t ctas = min(static_cast<int64_t>(a.ctas), total);
-  if (blockIdx.x >= ctas) return;
-  const int64_t e_first = total * blockIdx.x / ctas, e_end = total * (blockIdx.x + 1) / ctas;
-  int item = s_begin.item, entry = s_begin.entry;
-  int64_t e_at = e_first;
+  // rows that keep nothing
+  for (int n = blockIdx.x; n < a.items; n += gridDim.x) {
+    if (a.lists.count[list_of(a, n)] != 0) continue;
+    const int h0 = n % a.lists.tiles_h * kHeadTile, nh = min(G - h0, kHeadTile);
+    const int64_t head0 = static_cast<int64_t>(n / a.lists.tiles_h) * G + h0;
+    for (int i = tid; i < nh * D; i += kWarps * 32)
+      a.out[head0 * D + i] = __float2bfloat16_rn(0.f);
+    if (tid < nh && a.lse) a.lse[head0 + tid] = -INFINITY;
+  }
+  const Spread spread(s_begin.total, a.ctas);
+  const int e_first = spread.first(blockIdx.x), e_end = spread.first(blockIdx.x + 1);
+  int item = s_begin.item, entry = s_begin.entry, e_at = e_first;
 
   // this CTA's part of one item after the other
   for (; e_at < e_end; ++item, entry = 0) {
   const int n_item = a.lists.count[list_of(a, item)];
-  const int n_ent = static_cast<int>(min(static_cast<int64_t>(n_item - entry), e_end - e_at));
+  const int n_ent = min(n_item - entry, e_end - e_at);
   if (n_ent <= 0) continue;
   const bool whole = n_ent == n_item;
   const int slot = 2 * blockIdx.x + (e_at == e_first ? 0 : 1);
-  if (entry == 0 && tid == 0) a.start[item] = e_at;
+  const int e_item = e_at - entry;  // number of the item's first entry
   e_at += n_ent;
   const Entry* list = a.lists.list + static_cast<int64_t>(list_of(a, item)) * a.lists.most + entry;
   const int row = item / (a.c.Hkv * a.lists.tiles_h), kv = item / a.lists.tiles_h % a.c.Hkv;
@@ -780,78 +855,21 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
       finish(1u << h);
     }
   }
+  // ---- of an item in parts, the CTA that brings the last one joins them
+  if (!whole) {
+    __threadfence();
+    __syncthreads();
+    const int c0 = spread.cta_of(e_item), parts = spread.cta_of(e_item + n_item - 1) - c0 + 1;
+    if (tid == 0) s_last = atomicAdd(&a.lists.arrived[item], 1) == parts - 1;
+    __syncthreads();
+    if (s_last) {
+      __threadfence();
+      // the item is the first one of all its CTAs but, perhaps, the first
+      const int at0 = spread.first(c0) == e_item ? 0 : 1;
+      join_parts<D>(a, head0, nh, parts, [&](int s) { return 2 * (c0 + s) + (s == 0 ? at0 : 0); });
+    }
+  }
   __syncthreads();  // (the results in shared memory have been read)
-  }
-}
-
-// Joins the items that several CTAs have a part of (and writes those without a block): one CTA per
-// (row, query head). Threads first turn the parts' maxima into weights, then groups of D threads sum
-// the numerators of every kGroups-th part.
-constexpr int kJoinThreads = 256;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
-  constexpr int kGroups = kJoinThreads / D, kJoinWarps = kJoinThreads / 32;
-  extern __shared__ float weight[];  // ctas
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps], s_o[kGroups][D];
-  const int row = blockIdx.y, head = blockIdx.x, tid = threadIdx.x;
-  const int G = a.r.Hq / a.c.Hkv, h = head % G % kHeadTile;
-  const int item = (row * a.c.Hkv + head / G) * a.lists.tiles_h + head % G / kHeadTile;
-  const int64_t o_at = static_cast<int64_t>(row) * a.r.Hq + head;
-  cudaGridDependencySynchronize();
-  cudaTriggerProgrammaticLaunchCompletion();
-  const int n = a.lists.count[list_of(a, item)];
-  if (n == 0) {
-    if (tid < D) a.out[o_at * D + tid] = __float2bfloat16_rn(0.f);
-    if (tid == 0 && a.lse) a.lse[o_at] = -INFINITY;
-    return;
-  }
-  // CTA n takes entries total * n / N and up, so entry e is with CTA ((e + 1) N - 1) / total
-  const int64_t total = a.start[a.items], e0 = a.start[item];
-  const int64_t ctas = min(static_cast<int64_t>(a.ctas), total);
-  const int c0 = static_cast<int>(((e0 + 1) * ctas - 1) / total);
-  const int parts = static_cast<int>(((e0 + n) * ctas - 1) / total) - c0 + 1;
-  if (parts == 1) return;  // (its CTA has written the output)
-  const int first = total * c0 / ctas == e0 ? 0 : 1;  // the item is its first CTA's first or last
-  auto slot = [&](int s) { return 2 * (c0 + s) + (s == 0 ? first : 0); };
-  float m = -INFINITY;
-  for (int s = tid; s < parts; s += kJoinThreads) m = fmaxf(m, a.stat[slot(s) * kHeadTile + h].x);
-  for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  if (tid % 32 == 0) s_m[tid / 32] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, lx = 0.f;
-  for (int s = tid; s < parts; s += kJoinThreads) {
-    const float4 st = a.stat[slot(s) * kHeadTile + h];
-    const float f = exp2f(st.x - base);
-    weight[s] = f;
-    l = fmaf(f, st.y, l);
-    lx = fmaf(f, st.z, lx);
-  }
-  for (int o = 16; o; o /= 2) {
-    l += __shfl_xor_sync(kFull, l, o);
-    lx += __shfl_xor_sync(kFull, lx, o);
-  }
-  if (tid % 32 == 0) s_l[tid / 32] = l, s_x[tid / 32] = lx;
-  __syncthreads();
-  const int d = tid % D, grp = tid / D;
-  const float* part = a.part + static_cast<int64_t>(h) * D + d;
-  float x = 0.f;
-#pragma unroll 8
-  for (int s = grp; s < parts; s += kGroups)
-    x = fmaf(weight[s], part[static_cast<int64_t>(slot(s)) * kHeadTile * D], x);
-  s_o[grp][d] = x;
-  __syncthreads();
-  if (grp == 0) {
-    l = s_l[0], lx = s_x[0];
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) l += s_l[w], lx += s_x[w];
-#pragma unroll
-    for (int i = 1; i < kGroups; ++i) x += s_o[i][d];
-    a.out[o_at * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-    if (d == 0 && a.lse) a.lse[o_at] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
   }
 }
 
@@ -859,7 +877,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
 struct Sizes {
   int tiles_h, most, ctas;
   int64_t items, lists;
-  size_t list, count, start, stat, part, total;
+  size_t list, count, arrived, stat, part, total;
 };
 Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap, bool share) {
   Sizes s;
@@ -885,7 +903,7 @@ Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kc
   };
   s.list = take(sizeof(Entry) * static_cast<size_t>(s.lists) * s.most);
   s.count = take(sizeof(int32_t) * static_cast<size_t>(s.lists));
-  s.start = take(sizeof(int64_t) * static_cast<size_t>(s.items + 1));
+  s.arrived = take(sizeof(int32_t) * static_cast<size_t>(s.items));
   s.stat = take(sizeof(float4) * 2 * static_cast<size_t>(s.ctas) * kHeadTile);
   s.part = take(sizeof(float) * 2 * static_cast<size_t>(s.ctas) * kHeadTile * D);
   s.total = o;
@@ -908,10 +926,7 @@ cudaError_t launch(const Args& a, bool planned, cudaStream_t st) {
   e = cudaFuncSetAttribute(attn_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  e = launch_after(attn_kernel<FMT, D>, dim3(a.ctas), kWarps * 32, bytes, 1, st, a);
-  if (e != cudaSuccess) return e;
-  return launch_after(join_kernel<D>, dim3(a.r.Hq, a.r.R), kJoinThreads, sizeof(float) * a.ctas,
-                      1, st, a);
+  return launch_after(attn_kernel<FMT, D>, dim3(a.ctas), kWarps * 32, bytes, 1, st, a);
 }
 
 }  // namespace
@@ -922,6 +937,7 @@ DecodeLists decode_lists(const KvCache& c, int format, int D, const DecodeRows& 
   DecodeLists l;
   l.list = reinterpret_cast<Entry*>(ws + s.list);
   l.count = reinterpret_cast<int32_t*>(ws + s.count);
+  l.arrived = reinterpret_cast<int32_t*>(ws + s.arrived);
   l.most = s.most;
   l.tiles_h = s.tiles_h;
   return l;
@@ -938,7 +954,6 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   a.lists = decode_lists(c, format, D, r, share, ws);
   a.items = static_cast<int>(s.items);
   a.ctas = s.ctas;
-  a.start = reinterpret_cast<int64_t*>(ws + s.start);
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.stat = reinterpret_cast<float4*>(ws + s.stat);

@@ -42,6 +42,8 @@ constexpr int kDecodeHeads = 8;  // query heads of an item (columns of an MMA)
 struct DecodeLists {
   Entry* list = nullptr;
   int32_t* count = nullptr;
+  int32_t* arrived = nullptr;  // [items]: parts of the item that are there; whoever writes the lists
+                               // sets it to 0
   int most = 0;
   int tiles_h = 0;  // items of a kv head
 };

@@ -308,6 +308,9 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
 
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
+  if (rank == 0 && a.lists.list)
+    for (int n = tid; n < a.lists.tiles_h; n += kThreads)
+      a.lists.arrived[(static_cast<int64_t>(row) * a.c.Hkv + kv) * a.lists.tiles_h + n] = 0;
   int seq, len;
   decode_row(a.c, a.r, row, seq, len);
   const int last = (len + a.c.block - 1) / a.c.block - 1;
