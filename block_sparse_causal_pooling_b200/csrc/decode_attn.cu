@@ -40,8 +40,11 @@ namespace stem {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kWarps = 4;
 constexpr int kHeadTile = kDecodeHeads;
+constexpr int kMinEntries = 4;   // of a CTA, where fewer CTAs than fit then have work
+// Items in parts are joined by the CTA that brings the last part, which saves a launch, unless they
+// have more parts than this on average: then by a kernel of their own, with a CTA for each head.
+constexpr int kDirect = 16;
 constexpr int kStaged = 128;  // list entries in shared memory at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -58,7 +61,9 @@ struct Cfg {
   static constexpr bool Q = FMT != STEM_KV_BF16;
   static constexpr int TPS = Q ? 2 : 1;  // tiles a warp takes at once
   static constexpr int STAGES = FMT == STEM_KV_Q8 ? 2 : 3;
-  static constexpr int CTAS = FMT == STEM_KV_Q4 ? 4 : FMT == STEM_KV_Q8 ? 3 : 2;  // per SM, at least
+  static constexpr int WARPS = 4, THREADS = 32 * WARPS;
+  // CTAs an SM: as many as registers allow at 4 and 8 bits, and the rings at 16.
+  static constexpr int CTAS = FMT == STEM_KV_Q4 ? 4 : FMT == STEM_KV_Q8 ? 3 : 2;
   static constexpr int STEP = kKvTile * TPS;                                      // tokens
   static constexpr int STEP_BYTES = TPS * L::TILE_BYTES;
   static constexpr int RING = STAGES * STEP_BYTES;  // a warp's
@@ -135,14 +140,16 @@ struct Args {
   DecodeRows r;
   bool share;
   DecodeLists lists;
-  int items;  // R * Hkv * lists.tiles_h: a row, a kv head and up to 8 of its query heads
+  int items;  // a row, a kv head and up to 8 of its query heads each
   int ctas;
   __nv_bfloat16* out;
   float* lse;
-  // [2 * ctas][8] statistics (max in log2 units, sum for the output, sum for lse) and [D] numerators
-  // of the items that a CTA has a part of: its first one, and its last one
+  // Parts of items, two slots a CTA (its first item, and its last one): [slot][8] statistics (max in
+  // log2 units, sum for the output, sum for lse) and [slot][8][D] numerators.
   float4* stat;
   float* part;
+  bool direct;    // the CTA that brings an item's last part joins them
+  int32_t* start; // [items]: number of the item's first entry; [items]: total (where not direct)
 };
 
 // ------------------------------------------------------------------ the lists
@@ -235,8 +242,9 @@ struct Spread {
 struct Begin {
   int total, item, entry;
 };
+template <int WARPS>
 __device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int* wsum) {
-  const int tid = threadIdx.x, run = (a.items + kWarps * 32 - 1) / (kWarps * 32);
+  const int tid = threadIdx.x, run = (a.items + WARPS * 32 - 1) / (WARPS * 32);
   const int i0 = min(tid * run, a.items), i1 = min(i0 + run, a.items);
   int n = 0;
   for (int i = i0; i < i1; ++i) n += a.lists.count[list_of(a, i)];
@@ -248,7 +256,7 @@ __device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int* wsum) 
   if (tid % 32 == 31) wsum[tid / 32] = s;
   __syncthreads();
   int total = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < tid / 32) s += wsum[w];
     total += wsum[w];
   }
@@ -268,42 +276,69 @@ __device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int* wsum) 
   __syncthreads();
 }
 
-// Joins the parts of an item, once they are all there: a warp for each head, a lane for 4 channels
-// (at 64 channels the warp's halves take parts in turn). slot(s) is where part s is.
-template <int D, typename F>
-__device__ __forceinline__ void join_parts(const Args& a, int64_t head0, int nh, int parts, F slot) {
-  constexpr int kLanes = D / 4, kHalves = 32 / kLanes;
+// Joins parts of an item, once they are all there: a warp for each head, a lane for 4 channels (at
+// 64 channels the warp's halves take parts in turn). Part 0 is in slot slot0 + slot_first, part s in
+// slot0 + 2 s; st holds kJoinStaged statistics.
+constexpr int kJoinStaged = 512;
+
+// (Not inlined, and its loops mostly not unrolled: it runs once or twice in a CTA, and fetching
+// straight-line code for the first time costs more than running it.)
+template <int D, int WARPS>
+__device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, int parts,
+                                        float4* st, int slot0, int slot_first) {
+  auto slot = [&](int s) { return slot0 + 2 * s + (s == 0 ? slot_first : 0); };
+  constexpr int kLanes = D / 4, kHalves = 32 / kLanes, kAtOnce = 8;
   const int lane = threadIdx.x % 32, c = lane % kLanes, half = lane / kLanes;
-  for (int h = threadIdx.x / 32; h < nh; h += kWarps) {
-    float m = -INFINITY;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, __ldcg(&a.stat[slot(s) * kHeadTile + h]).x);
-    for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, lx = 0.f;
+  const int most = kJoinStaged / nh;  // parts staged at a time
+  for (int h0 = 0; h0 < nh; h0 += WARPS) {
+    const int h = min(h0 + static_cast<int>(threadIdx.x) / 32, nh - 1);  // (the last one twice)
+    float m = -INFINITY, l = 0.f, lx = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-      float f = 0.f;
-      if (s0 + lane < parts) {
-        const float4 st = __ldcg(&a.stat[slot(s0 + lane) * kHeadTile + h]);
-        f = exp2f(st.x - base);
-        l = fmaf(f, st.y, l);
-        lx = fmaf(f, st.z, lx);
+#pragma unroll 1
+    for (int s0 = 0; s0 < parts; s0 += most) {
+      const int n = min(parts - s0, most);
+      __syncthreads();
+#pragma unroll 1
+      for (int i = threadIdx.x; i < n * nh; i += WARPS * 32)
+        st[i] = __ldcg(&a.stat[slot(s0 + i / nh) * kHeadTile + i % nh]);
+      __syncthreads();
+      float top = m;
+#pragma unroll 1
+      for (int s = lane; s < n; s += 32) top = fmaxf(top, st[s * nh + h].x);
+#pragma unroll
+      for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      const float base = top == -INFINITY ? 0.f : top, f0 = ex2(m - base);
+      m = top;
+      l *= f0, lx *= f0;
+      x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
+#pragma unroll 1
+      for (int s = lane; s < n; s += 32) {
+        const float4 v = st[s * nh + h];
+        const float f = ex2(v.x - base);
+        l = fmaf(f, v.y, l);
+        lx = fmaf(f, v.z, lx);
       }
-      const int n = min(parts - s0, 32);
-#pragma unroll 8
-      for (int i = 0; i < n; i += kHalves) {
-        const int e = i + half;
-        const float w = __shfl_sync(kFull, f, e & 31);
-        if (e < n) {
-          const float4 p = __ldcg(reinterpret_cast<const float4*>(
-                                      a.part + (static_cast<int64_t>(slot(s0 + e)) * kHeadTile + h) * D) + c);
-          x.x = fmaf(w, p.x, x.x);
-          x.y = fmaf(w, p.y, x.y);
-          x.z = fmaf(w, p.z, x.z);
-          x.w = fmaf(w, p.w, x.w);
+#pragma unroll 1
+      for (int i0 = half; i0 < n; i0 += kAtOnce * kHalves) {
+        float4 p[kAtOnce];
+        const float4* src = reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(h) * D) + c;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {  // (past the end: the last part again, with weight 0)
+          const int e = min(i0 + i * kHalves, n - 1);
+          p[i] = __ldcg(src + static_cast<int64_t>(slot(s0 + e)) * (kHeadTile * D / 4));
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int e = i0 + i * kHalves;
+          const float f = e < n ? ex2(st[min(e, n - 1) * nh + h].x - base) : 0.f;
+          x.x = fmaf(f, p[i].x, x.x);
+          x.y = fmaf(f, p[i].y, x.y);
+          x.z = fmaf(f, p[i].z, x.z);
+          x.w = fmaf(f, p[i].w, x.w);
         }
       }
     }
+#pragma unroll
     for (int o = 16; o; o /= 2) {
       l += __shfl_xor_sync(kFull, l, o);
       lx += __shfl_xor_sync(kFull, lx, o);
@@ -323,33 +358,34 @@ __device__ __forceinline__ void join_parts(const Args& a, int64_t head0, int nh,
 }
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(const Args a) {
+__global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_kernel(const Args a) {
   using L = Kv<FMT, D>;
   using C = Cfg<FMT, D>;
   constexpr bool kQuant = C::Q;
   constexpr int NG = L::NG, TPS = C::TPS;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Begin s_begin;
-  __shared__ int s_sum[kWarps];
+  __shared__ int s_sum[C::WARPS];
   __shared__ bool s_last;
   __shared__ Entry ent[kStaged];
-  __shared__ float s_m[kWarps][kHeadTile], s_l[kWarps][kHeadTile], s_x[kWarps][kHeadTile];
+  __shared__ float s_m[C::WARPS][kHeadTile], s_l[C::WARPS][kHeadTile], s_x[C::WARPS][kHeadTile];
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int G = a.r.Hq / a.c.Hkv;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
-  find_begin(a, &s_begin, s_sum);
+  find_begin<C::WARPS>(a, &s_begin, s_sum);
   // rows that keep nothing
   for (int n = blockIdx.x; n < a.items; n += gridDim.x) {
     if (a.lists.count[list_of(a, n)] != 0) continue;
     const int h0 = n % a.lists.tiles_h * kHeadTile, nh = min(G - h0, kHeadTile);
     const int64_t head0 = static_cast<int64_t>(n / a.lists.tiles_h) * G + h0;
-    for (int i = tid; i < nh * D; i += kWarps * 32)
+    for (int i = tid; i < nh * D; i += C::THREADS)
       a.out[head0 * D + i] = __float2bfloat16_rn(0.f);
     if (tid < nh && a.lse) a.lse[head0 + tid] = -INFINITY;
   }
   const Spread spread(s_begin.total, a.ctas);
+  if (!a.direct && blockIdx.x == 0 && tid == 0) a.start[a.items] = s_begin.total;
   const int e_first = spread.first(blockIdx.x), e_end = spread.first(blockIdx.x + 1);
   int item = s_begin.item, entry = s_begin.entry, e_at = e_first;
 
@@ -370,6 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
   int seq, len;
   decode_row(a.c, a.r, row, seq, len);
 
+  float* o_s = reinterpret_cast<float*>(smem);  // [C::WARPS][8][D], over the rings at the end
   // ---- the queries, as B operands: head g, channels 8t .. 8t + 7 of each group
   uint32_t qf[NG][4];
   {
@@ -381,44 +418,46 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
       qf[y][0] = u.x, qf[y][1] = u.y, qf[y][2] = u.z, qf[y][3] = u.w;
     }
   }
-  float* o_s = reinterpret_cast<float*>(smem);  // [kWarps][8][D], over the rings at the end
   float qscale = kLog2e / sqrtf(static_cast<float>(D));  // of head g: logits in log2 units
-  uint32_t ob0 = 0, ob1 = 0;  // B operand of the offsets' MMA (below)
+  float off[NG];
   if constexpr (kQuant) {
-    uint32_t top = 0;
+    uint32_t top = 0;  // largest |q|: bf16 bits order like the numbers, two at a time
 #pragma unroll
     for (int y = 0; y < NG; ++y)
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        top = max(top, max(qf[y][n] & 0x7fffu, qf[y][n] >> 16 & 0x7fffu));
+      for (int n = 0; n < 4; ++n) top = __vmaxu2(top, qf[y][n] & 0x7fff7fffu);
+    top = max(top & 0xffffu, top >> 16);
     top = max(top, __shfl_xor_sync(kFull, top, 1));
     top = max(top, __shfl_xor_sync(kFull, top, 2));
-    // exponent that brings the largest |q| to [2^14, 2^15); at least -100, so that what undoes it
-    // stays a float32
+    // exponent that brings the largest |q| to [2^14, 2^15); within +-100, so that it and what
+    // undoes it are float32 numbers
     const int up = top < 0x0080u || top >= 0x7f80u
                        ? 0
-                       : max(14 - (static_cast<int>(top >> 7) - 127), -100);
-    qscale *= ldexpf(1.f, min(24 - up, 126));
-    const float up1 = ldexpf(1.f, up / 2), up2 = ldexpf(1.f, up - up / 2);
-    float off[NG];
+                       : min(max(14 - (static_cast<int>(top >> 7) - 127), -100), 100);
+    qscale *= __uint_as_float(static_cast<uint32_t>(127 + 24 - up) << 23);
+    const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 #pragma unroll
     for (int y = 0; y < NG; ++y) {
       float sum = 0.f;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const __half2 h = __floats2half2_rn(low16(qf[y][n]) * up1 * up2,
-                                            high16(qf[y][n]) * up1 * up2);
-        sum += __low2float(h) + __high2float(h);
-        // odd words meet upper nibbles, which weigh 16 times as much
-        const __half2 w = FMT == STEM_KV_Q4 && (n & 1)
-                              ? __hmul2(h, __floats2half2_rn(0.0625f, 0.0625f))
-                              : h;
-        qf[y][n] = *reinterpret_cast<const uint32_t*>(&w);
+        const float x0 = low16(qf[y][n]) * f, x1 = high16(qf[y][n]) * f;
+        // (fp16 holds both exactly, but for entries 2^-30 of the largest)
+        sum += x0 + x1;
+        qf[y][n] = pack_f16(x0, x1);
+        if (FMT == STEM_KV_Q4 && (n & 1)) {  // meets upper nibbles, which weigh 16 times as much
+          const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&qf[y][n]),
+                                    __floats2half2_rn(0.0625f, 0.0625f));
+          qf[y][n] = *reinterpret_cast<const uint32_t*>(&h);
+        }
       }
       sum += __shfl_xor_sync(kFull, sum, 1);
       sum += __shfl_xor_sync(kFull, sum, 2);
       off[y] = -static_cast<float>(L::OFFSET) * 0x1p-24f * sum;
     }
+  }
+  uint32_t ob0 = 0, ob1 = 0;  // B operand of the offsets' MMA
+  if constexpr (kQuant) {
     // What the codes' offset adds to a logit, sum_y s_ty off_yh, is one MMA of the scales as they
     // are (bf16) with off in three bf16 pieces along k: groups (0, 1), (2, 3) or, of 64 channels,
     // (0, 1) alone, from lane t = 0 on.
@@ -444,8 +483,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
   float m0, m1, l0, l1;  // running maximum (log2 units) and sum of the weights as the MMA sees them
   float lim0, lim1;      // largest logits (as the MMA gives them) within the maximum's slack
   float x0, x1;          // at 16 bits: sum of the weights before rounding
-  float vf;              // power of two of the V scales
-  int vlim;              // largest scale (bf16 bits) that vf is good for
+  float vf0, vf1;        // power of two of the V scales that each head meets
+  int vlim0, vlim1;      // largest scales (bf16 bits) that they are good for
   unsigned char* ring = smem + warp * C::RING;
   const int spb_log = a.c.block / C::STEP == 2 ? 1 : a.c.block / C::STEP == 4 ? 2 : 3;
   const int64_t page_bytes = static_cast<int64_t>(a.c.Hkv) * a.c.record;
@@ -461,17 +500,17 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
     for (int e = 0; e < 4; ++e) asum[e] = 0.f;
     m0 = m1 = lim0 = lim1 = -INFINITY;
     l0 = l1 = x0 = x1 = 0.f;
-    vf = 1.f;
-    vlim = -1;
+    vf0 = vf1 = 1.f;
+    vlim0 = vlim1 = -1;
     for (int e0 = 0; e0 < n_ent; e0 += kStaged) {
     __syncthreads();
     const int n_now = min(n_ent - e0, kStaged);
-    for (int n = tid; n < n_now; n += kWarps * 32) ent[n] = list[e0 + n];
+    for (int n = tid; n < n_now; n += C::THREADS) ent[n] = list[e0 + n];
     __syncthreads();
     // Warp w takes steps [u0, u1) of the staged entries, one after the other: two walkers, one
     // that fetches and one that computes, look at an entry when they come to it.
     const int units = n_now << spb_log, per_entry = 1 << spb_log;
-    const int u0 = units * warp / kWarps, u1 = units * (warp + 1) / kWarps;
+    const int u0 = units * warp / C::WARPS, u1 = units * (warp + 1) / C::WARPS;
     auto tokens = [&](const Entry& e) -> int {  // of an entry; 0 or less: nothing to do
       return e.what >> 16 & heads ? len - static_cast<int>(e.what & 0xffffu) * a.c.block : 0;
     };
@@ -517,66 +556,67 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
         // ---- logits: rows are tokens g and g + 8 of a tile, columns heads 2t and 2t + 1
         float z[TPS][4];
         uint32_t sv[TPS][2][2];  // V scales of tokens g, g + 8: two groups a word
+        if constexpr (!kQuant) {
 #pragma unroll
-        for (int i = 0; i < TPS; ++i) {
-          const unsigned char* tile = step + i * L::TILE_BYTES;
-          if constexpr (!kQuant) {
+          for (int y = 0; y < NG; ++y) {
+            const uint4 ka = *reinterpret_cast<const uint4*>(step + L::word(0, y, 0, lane));
+            const uint4 kb = *reinterpret_cast<const uint4*>(step + L::word(1, y, 0, lane));
+            if (y == 0)
+              mma_bf16_new(z[0], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
+            else
+              mma_bf16(z[0], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
+            mma_bf16(z[0], ka.z, kb.z, ka.w, kb.w, qf[y][2], qf[y][3]);
+          }
+        } else {
+          uint32_t kw[TPS][2][NG * L::WPG], sk[TPS][2][2];
 #pragma unroll
-            for (int y = 0; y < NG; ++y) {
-              const uint4 ka = *reinterpret_cast<const uint4*>(tile + L::word(0, y, 0, lane));
-              const uint4 kb = *reinterpret_cast<const uint4*>(tile + L::word(1, y, 0, lane));
-              if (y == 0)
-                mma_bf16_new(z[i], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
-              else
-                mma_bf16(z[i], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
-              mma_bf16(z[i], ka.z, kb.z, ka.w, kb.w, qf[y][2], qf[y][3]);
+          for (int i = 0; i < TPS; ++i) {
+            const unsigned char* tile = step + i * L::TILE_BYTES;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const unsigned char* s = tile + 2 * L::CODES + (g + 8 * r) * L::SCROW;
+              if constexpr (NG == 4) {
+                const uint4 x = *reinterpret_cast<const uint4*>(s);
+                sk[i][r][0] = x.x, sk[i][r][1] = x.y, sv[i][r][0] = x.z, sv[i][r][1] = x.w;
+              } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(s);
+                sk[i][r][0] = x.x, sv[i][r][0] = x.y;
+                sk[i][r][1] = sv[i][r][1] = 0;
+              }
             }
-          } else {
-            uint32_t kw[2][NG * L::WPG], sk[2][2];
+            const uint32_t s0 = NG == 4 && (t & 1) ? sk[i][0][1] : sk[i][0][0];
+            const uint32_t s1 = NG == 4 && (t & 1) ? sk[i][1][1] : sk[i][1][0];
+            mma_bf16_new(z[i], s0, s1, s0, s1, ob0, ob1);
 #pragma unroll
             for (int p = 0; p < L::PIECES; ++p) {
               const uint4 x = *reinterpret_cast<const uint4*>(tile + p * 512 + lane * 16);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int n = 0; n < 4; ++n)
-                kw[(p * 4 + n) / (NG * L::WPG)][(p * 4 + n) % (NG * L::WPG)] = w[n];
+                kw[i][(p * 4 + n) / (NG * L::WPG)][(p * 4 + n) % (NG * L::WPG)] = w[n];
             }
+          }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const unsigned char* s = tile + 2 * L::CODES + (g + 8 * r) * L::SCROW;
-              if constexpr (NG == 4) {
-                const uint4 x = *reinterpret_cast<const uint4*>(s);
-                sk[r][0] = x.x, sk[r][1] = x.y, sv[i][r][0] = x.z, sv[i][r][1] = x.w;
-              } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(s);
-                sk[r][0] = x.x, sv[i][r][0] = x.y;
-                sk[r][1] = sv[i][r][1] = 0;
-              }
-            }
-            {
-              const uint32_t s0 = NG == 4 && (t & 1) ? sk[0][1] : sk[0][0];
-              const uint32_t s1 = NG == 4 && (t & 1) ? sk[1][1] : sk[1][0];
-              mma_bf16_new(z[i], s0, s1, s0, s1, ob0, ob1);
-            }
+          for (int y = 0; y < NG; ++y) {
 #pragma unroll
-            for (int y = 0; y < NG; ++y) {
+            for (int i = 0; i < TPS; ++i) {
               float d[4];
               if constexpr (FMT == STEM_KV_Q4) {
-                const uint32_t a0 = kw[0][y], a1 = kw[1][y];
-                mma_f16_new(d, a0 & 0x000f000fu, a1 & 0x000f000fu,
-                             a0 & 0x00f000f0u, a1 & 0x00f000f0u, qf[y][0], qf[y][1]);
+                const uint32_t a0 = kw[i][0][y], a1 = kw[i][1][y];
+                mma_f16_new(d, a0 & 0x000f000fu, a1 & 0x000f000fu, a0 & 0x00f000f0u,
+                            a1 & 0x00f000f0u, qf[y][0], qf[y][1]);
                 mma_f16(d, a0 >> 8 & 0x000f000fu, a1 >> 8 & 0x000f000fu, a0 >> 8 & 0x00f000f0u,
                         a1 >> 8 & 0x00f000f0u, qf[y][2], qf[y][3]);
               } else {
-                const uint32_t a0 = kw[0][2 * y], a1 = kw[1][2 * y];
-                const uint32_t b0 = kw[0][2 * y + 1], b1 = kw[1][2 * y + 1];
-                mma_f16_new(d, a0 & 0x00ff00ffu, a1 & 0x00ff00ffu,
-                             a0 >> 8 & 0x00ff00ffu, a1 >> 8 & 0x00ff00ffu, qf[y][0], qf[y][1]);
+                const uint32_t a0 = kw[i][0][2 * y], a1 = kw[i][1][2 * y];
+                const uint32_t b0 = kw[i][0][2 * y + 1], b1 = kw[i][1][2 * y + 1];
+                mma_f16_new(d, a0 & 0x00ff00ffu, a1 & 0x00ff00ffu, a0 >> 8 & 0x00ff00ffu,
+                            a1 >> 8 & 0x00ff00ffu, qf[y][0], qf[y][1]);
                 mma_f16(d, b0 & 0x00ff00ffu, b1 & 0x00ff00ffu, b0 >> 8 & 0x00ff00ffu,
                         b1 >> 8 & 0x00ff00ffu, qf[y][2], qf[y][3]);
               }
-              const float s0 = y & 1 ? high16(sk[0][y / 2]) : low16(sk[0][y / 2]);
-              const float s1 = y & 1 ? high16(sk[1][y / 2]) : low16(sk[1][y / 2]);
+              const float s0 = y & 1 ? high16(sk[i][0][y / 2]) : low16(sk[i][0][y / 2]);
+              const float s1 = y & 1 ? high16(sk[i][1][y / 2]) : low16(sk[i][1][y / 2]);
               z[i][0] = fmaf(s0, d[0], z[i][0]);
               z[i][1] = fmaf(s0, d[1], z[i][1]);
               z[i][2] = fmaf(s1, d[2], z[i][2]);
@@ -586,8 +626,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
         }
         // ---- tokens past the row's length and heads that do not keep the block: weight 0, and
         // scale 0, whatever their bytes hold
+        bool on0 = true, on1 = true;
         if (valid < C::STEP || hb != 0xffu) {
-          const bool on0 = hb >> (2 * t) & 1, on1 = hb >> (2 * t + 1) & 1;
+          on0 = hb >> (2 * t) & 1;
+          on1 = hb >> (2 * t + 1) & 1;
 #pragma unroll
           for (int i = 0; i < TPS; ++i)
 #pragma unroll
@@ -609,7 +651,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
           if constexpr (NG == 4)
             top = __vmaxu2(top, __vmaxu2(__vmaxu2(sv[0][0][1], sv[0][1][1]),
                                          __vmaxu2(sv[1][0][1], sv[1][1][1])));
-          move = static_cast<int>(max(top & 0xffffu, top >> 16)) > vlim;
+          const int most = static_cast<int>(max(top & 0xffffu, top >> 16));
+          move = (on0 && most > vlim0) || (on1 && most > vlim1);
         }
         move |= n0 > lim0 || n1 > lim1;
         if (__any_sync(kFull, move)) {
@@ -644,15 +687,18 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
                   top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
                 }
             top = __reduce_max_sync(kFull, top);
-            if (static_cast<int>(top) > vlim) {
-              const uint32_t ex = top >> 7;  // biased exponent
-              const float f = __uint_as_float(min(254u + kScaleSet - ex, 245u) << 23);
-              if (vlim >= 0) {
-                c0 *= f / vf;
-                c1 *= f / vf;
-              }
-              vf = f;
-              vlim = static_cast<int>((ex + kScaleSlack + 1) << 7) - 1;
+            const uint32_t ex = top >> 7;  // biased exponent
+            const float f = __uint_as_float(min(254u + kScaleSet - ex, 245u) << 23);
+            const int lim = static_cast<int>((ex + kScaleSlack + 1) << 7) - 1;
+            if (on0 && static_cast<int>(top) > vlim0) {
+              if (vlim0 >= 0) c0 *= f / vf0;
+              vf0 = f;
+              vlim0 = lim;
+            }
+            if (on1 && static_cast<int>(top) > vlim1) {
+              if (vlim1 >= 0) c1 *= f / vf1;
+              vf1 = f;
+              vlim1 = lim;
             }
           }
 #pragma unroll
@@ -714,7 +760,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
             l0 += p[i][0] + p[i][2];
             l1 += p[i][1] + p[i][3];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) p[i][n] *= vf;
+            for (int n = 0; n < 4; ++n) p[i][n] *= n & 1 ? vf1 : vf0;
 #pragma unroll
             for (int q = 0; q < L::PIECES; ++q) {
               const uint4 x = *reinterpret_cast<const uint4*>(step + i * L::TILE_BYTES + L::CODES +
@@ -763,7 +809,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
 
     // ---- numerators in units of V: o = sum_t p_t V_t relative to 2^m
     if constexpr (kQuant) {
-      const float inv = 1.f / vf;
+      const float inv0 = 1.f / vf0, inv1 = 1.f / vf1;
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
         const float off0 = static_cast<float>(L::OFFSET) * __shfl_sync(kFull, asum[0], 4 * y + t);
@@ -772,10 +818,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
         const float second = FMT == STEM_KV_Q4 ? 0x1p20f : 0x1p24f;
 #pragma unroll
         for (int n = 2 * y; n < 2 * y + 2; ++n) {
-          acc[n][0] = (acc[n][0] * 0x1p24f - off0) * inv;
-          acc[n][1] = (acc[n][1] * 0x1p24f - off1) * inv;
-          acc[n][2] = (acc[n][2] * second - off0) * inv;
-          acc[n][3] = (acc[n][3] * second - off1) * inv;
+          acc[n][0] = (acc[n][0] * 0x1p24f - off0) * inv0;
+          acc[n][1] = (acc[n][1] * 0x1p24f - off1) * inv1;
+          acc[n][2] = (acc[n][2] * second - off0) * inv0;
+          acc[n][3] = (acc[n][3] * second - off1) * inv1;
         }
       }
       x0 = l0;
@@ -808,28 +854,48 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
           make_float4(acc[2 * y][1], acc[2 * y][3], acc[2 * y + 1][1], acc[2 * y + 1][3]);
     }
     __syncthreads();
-    for (int n = tid; n < nh * D; n += kWarps * 32) {
-      const int h = n / D, d = n % D;
-      if (!(heads >> h & 1)) continue;
-      float m = s_m[0][h];
+    // each head's warps' weights, relative to the largest maximum, in place of their maxima
+    if (tid < kHeadTile) {
+      float m = s_m[0][tid];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_m[w][h]);
+      for (int w = 1; w < C::WARPS; ++w) m = fmaxf(m, s_m[w][tid]);
       const float base = m == -INFINITY ? 0.f : m;
-      float x = 0.f, l = 0.f, lx = 0.f;
+      float l = 0.f, lx = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (s_m[w][h] == -INFINITY && s_l[w][h] == 0.f) continue;  // saw nothing of this head
-        const float f = exp2f(s_m[w][h] - base);
-        x = fmaf(f, o_s[(w * kHeadTile + h) * D + d], x);
-        l = fmaf(f, s_l[w][h], l);
-        lx = fmaf(f, s_x[w][h], lx);
+      for (int w = 0; w < C::WARPS; ++w) {  // (a warp that saw nothing of the head weighs 0)
+        const float f = ex2(s_m[w][tid] - base);
+        s_m[w][tid] = f;
+        l = fmaf(f, s_l[w][tid], l);
+        lx = fmaf(f, s_x[w][tid], lx);
+      }
+      if (heads >> tid & 1) {
+        s_l[0][tid] = l == 0.f ? 0.f : 1.f / l;
+        if (!whole)
+          a.stat[slot * kHeadTile + tid] = make_float4(m, l, lx, 0.f);
+        else if (a.lse && tid < nh)
+          a.lse[head0 + tid] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+      }
+    }
+    __syncthreads();
+    for (int n = tid; n < nh * (D / 4); n += C::THREADS) {
+      const int h = n / (D / 4), d = n % (D / 4);
+      if (!(heads >> h & 1)) continue;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) {
+        const float f = s_m[w][h];
+        const float4 v = reinterpret_cast<const float4*>(o_s + (w * kHeadTile + h) * D)[d];
+        x.x = fmaf(f, v.x, x.x);
+        x.y = fmaf(f, v.y, x.y);
+        x.z = fmaf(f, v.z, x.z);
+        x.w = fmaf(f, v.w, x.w);
       }
       if (whole) {
-        a.out[(head0 + h) * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-        if (d == 0 && a.lse) a.lse[head0 + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+        const float inv = s_l[0][h];
+        reinterpret_cast<uint2*>(a.out + (head0 + h) * D)[d] =
+            make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
       } else {
-        a.part[(static_cast<int64_t>(slot) * kHeadTile + h) * D + d] = x;
-        if (d == 0) a.stat[slot * kHeadTile + h] = make_float4(m, l, lx, 0.f);
+        reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(slot) * kHeadTile + h) * D)[d] = x;
       }
     }
   };
@@ -856,20 +922,85 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
     }
   }
   // ---- of an item in parts, the CTA that brings the last one joins them
-  if (!whole) {
+  if (!whole && a.direct) {
+    const int c0 = spread.cta_of(e_item), parts = spread.cta_of(e_item + n_item - 1) - c0 + 1;
     __threadfence();
     __syncthreads();
-    const int c0 = spread.cta_of(e_item), parts = spread.cta_of(e_item + n_item - 1) - c0 + 1;
     if (tid == 0) s_last = atomicAdd(&a.lists.arrived[item], 1) == parts - 1;
     __syncthreads();
     if (s_last) {
-      __threadfence();
-      // the item is the first one of all its CTAs but, perhaps, the first
-      const int at0 = spread.first(c0) == e_item ? 0 : 1;
-      join_parts<D>(a, head0, nh, parts, [&](int s) { return 2 * (c0 + s) + (s == 0 ? at0 : 0); });
+      __threadfence();  // (the other CTAs' parts are visible)
+      // the item is the first one of all its CTAs but, perhaps, c0
+      join_parts<D, C::WARPS>(a, head0, nh, parts, reinterpret_cast<float4*>(smem), 2 * c0,
+                              spread.first(c0) == e_item ? 0 : 1);
     }
+  } else if (!a.direct && entry == 0 && tid == 0) {
+    a.start[item] = e_item;
   }
   __syncthreads();  // (the results in shared memory have been read)
+  }
+}
+
+// Joins the items that several CTAs have a part of: one CTA per (row, query head). Threads first turn
+// the parts' maxima into weights, then groups of D threads sum the numerators of every kGroups-th part.
+constexpr int kJoinThreads = 512;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
+  constexpr int kGroups = kJoinThreads / D, kJoinWarps = kJoinThreads / 32;
+  extern __shared__ float weight[];  // ctas
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps], s_o[kGroups][D];
+  const int row = blockIdx.y, head = blockIdx.x, tid = threadIdx.x;
+  const int G = a.r.Hq / a.c.Hkv, h = head % G % kHeadTile;
+  const int item = (row * a.c.Hkv + head / G) * a.lists.tiles_h + head % G / kHeadTile;
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int n = a.lists.count[list_of(a, item)];
+  if (n == 0) return;
+  const Spread spread(a.start[a.items], a.ctas);
+  const int e0 = a.start[item], c0 = spread.cta_of(e0), parts = spread.cta_of(e0 + n - 1) - c0 + 1;
+  if (parts == 1) return;  // (its CTA has written the output)
+  const int first = spread.first(c0) == e0 ? 0 : 1;  // the item is its first CTA's first or last
+  auto slot = [&](int s) { return 2 * (c0 + s) + (s == 0 ? first : 0); };
+  float m = -INFINITY;
+  for (int s = tid; s < parts; s += kJoinThreads) m = fmaxf(m, a.stat[slot(s) * kHeadTile + h].x);
+  for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  if (tid % 32 == 0) s_m[tid / 32] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f, lx = 0.f;
+  for (int s = tid; s < parts; s += kJoinThreads) {
+    const float4 st = a.stat[slot(s) * kHeadTile + h];
+    const float f = ex2(st.x - base);
+    weight[s] = f;
+    l = fmaf(f, st.y, l);
+    lx = fmaf(f, st.z, lx);
+  }
+  for (int o = 16; o; o /= 2) {
+    l += __shfl_xor_sync(kFull, l, o);
+    lx += __shfl_xor_sync(kFull, lx, o);
+  }
+  if (tid % 32 == 0) s_l[tid / 32] = l, s_x[tid / 32] = lx;
+  __syncthreads();
+  const int d = tid % D, grp = tid / D;
+  const float* part = a.part + static_cast<int64_t>(h) * D + d;
+  float x = 0.f;
+#pragma unroll 8
+  for (int s = grp; s < parts; s += kGroups)
+    x = fmaf(weight[s], part[static_cast<int64_t>(slot(s)) * kHeadTile * D], x);
+  s_o[grp][d] = x;
+  __syncthreads();
+  if (grp == 0) {
+    l = s_l[0], lx = s_x[0];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) l += s_l[w], lx += s_x[w];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) x += s_o[i][d];
+    const int64_t o = static_cast<int64_t>(row) * a.r.Hq + head;
+    a.out[o * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
+    if (d == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
   }
 }
 
@@ -877,7 +1008,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<FMT, D>::CTAS) attn_kernel(co
 struct Sizes {
   int tiles_h, most, ctas;
   int64_t items, lists;
-  size_t list, count, arrived, stat, part, total;
+  size_t list, count, arrived, start, stat, part, total;
 };
 Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap, bool share) {
   Sizes s;
@@ -889,12 +1020,13 @@ Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kc
   s.most = share ? kcap
                  : static_cast<int>(std::min<int64_t>(
                        static_cast<int64_t>(std::min(G, kHeadTile)) * kcap, max_blocks));
-  // as many CTAs as run at once, so that each gets the same number of blocks
+  // as many CTAs as run at once, so that each gets the same number of blocks; fewer where that
+  // would be less than kMinEntries each
   const int per_sm = format == STEM_KV_Q4 ? Cfg<STEM_KV_Q4, 128>::CTAS
                      : format == STEM_KV_Q8 ? Cfg<STEM_KV_Q8, 128>::CTAS
                                             : Cfg<STEM_KV_BF16, 128>::CTAS;
   s.ctas = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(sm_count()) * per_sm,
-                                              s.items * s.most));
+                                              (s.items * s.most + kMinEntries - 1) / kMinEntries));
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -903,9 +1035,11 @@ Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kc
   };
   s.list = take(sizeof(Entry) * static_cast<size_t>(s.lists) * s.most);
   s.count = take(sizeof(int32_t) * static_cast<size_t>(s.lists));
+  const size_t slots = 2 * static_cast<size_t>(s.ctas);
   s.arrived = take(sizeof(int32_t) * static_cast<size_t>(s.items));
-  s.stat = take(sizeof(float4) * 2 * static_cast<size_t>(s.ctas) * kHeadTile);
-  s.part = take(sizeof(float) * 2 * static_cast<size_t>(s.ctas) * kHeadTile * D);
+  s.start = take(sizeof(int32_t) * static_cast<size_t>(s.items + 1));
+  s.stat = take(sizeof(float4) * slots * kHeadTile);
+  s.part = take(sizeof(float) * slots * kHeadTile * D);
   s.total = o;
   return s;
 }
@@ -913,7 +1047,8 @@ Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kc
 template <int FMT, int D>
 cudaError_t launch(const Args& a, bool planned, cudaStream_t st) {
   using C = Cfg<FMT, D>;
-  static_assert(C::RING >= kHeadTile * D * 4, "the rings hold the warps' results at the end");
+  static_assert(C::RING >= kHeadTile * D * 4 && C::WARPS * C::RING >= kJoinStaged * 16,
+                "the rings hold the warps' results, then the parts' statistics, at the end");
   cudaError_t e = cudaSuccess;
   if (!planned) {
     const size_t mask = a.share ? 0 : 4 * ((a.c.max_blocks + 3) / 4);
@@ -921,12 +1056,15 @@ cudaError_t launch(const Args& a, bool planned, cudaStream_t st) {
     e = launch_after(plan_kernel, dim3(lists, a.r.R), kPlanThreads, mask, 1, st, a);
     if (e != cudaSuccess) return e;
   }
-  constexpr size_t bytes = static_cast<size_t>(kWarps) * C::RING;
+  constexpr size_t bytes = static_cast<size_t>(C::WARPS) * C::RING;
   // (per device and context; 0.1 us)
   e = cudaFuncSetAttribute(attn_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  return launch_after(attn_kernel<FMT, D>, dim3(a.ctas), kWarps * 32, bytes, 1, st, a);
+  e = launch_after(attn_kernel<FMT, D>, dim3(a.ctas), C::THREADS, bytes, 1, st, a);
+  if (e != cudaSuccess || a.direct) return e;
+  return launch_after(join_kernel<D>, dim3(a.r.Hq, a.r.R), kJoinThreads, sizeof(float) * a.ctas, 1,
+                      st, a);
 }
 
 }  // namespace
@@ -956,6 +1094,8 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   a.ctas = s.ctas;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
+  a.direct = s.ctas <= kDirect * s.items;
+  a.start = reinterpret_cast<int32_t*>(ws + s.start);
   a.stat = reinterpret_cast<float4*>(ws + s.stat);
   a.part = reinterpret_cast<float*>(ws + s.part);
   if (D == 128) {
