@@ -4,7 +4,8 @@
 
 Every .cu / .cpp under csrc/ is compiled separately (in parallel) into _build/, then linked
 into block_sparse_causal_pooling_b200/libstem.so with the CUDA runtime linked statically.
-`-Xptxas -v` resource usage is written to _build/ptxas.log.
+csrc/python/ becomes the extension module _decode.so (g++, against torch's headers), the native part
+of the decode binding, which calls libstem.so beside it. `-Xptxas -v` resource usage is written to _build/ptxas.log.
 """
 
 from __future__ import annotations
@@ -21,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libstem.so")
+BIND = os.path.join(PKG, "_decode.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -64,11 +66,44 @@ def _compile(src: str, verbose: bool) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _build_binding(force: bool) -> None:
+    src = os.path.join(CSRC, "python", "decode_bind.cpp")
+    if not force and not _stale(BIND, [src, os.path.join(INCLUDE, "stem.h"), LIB]):
+        return
+    import sysconfig
+
+    import torch
+
+    troot = os.path.dirname(os.path.abspath(torch.__file__))
+    tinc, tlib = os.path.join(troot, "include"), os.path.join(troot, "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    incs = [INCLUDE, tinc, os.path.join(tinc, "torch", "csrc", "api", "include"),
+            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BIND + ".tmp"
+    # (torch's own libraries are in the process before this module is: no run path to them)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for i in incs:
+        cmd += ["-I", i]
+    cmd += ["-o", tmp, src, "-L", PKG, "-l:libstem.so", "-L", tlib, "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for decode_bind.cpp:\n" + r.stderr)
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_library(force, verbose)
+    _build_binding(force)
+    return LIB
+
+
+def _build_library(force: bool, verbose: bool) -> None:
     srcs = _sources()
     deps = srcs + _headers() + [os.path.abspath(__file__)]
     if not force and not _stale(LIB, deps):
-        return LIB
+        return
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         results = list(ex.map(lambda s: _compile(s, verbose), srcs))
@@ -81,7 +116,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stderr)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -118,10 +118,10 @@ class stem_cache_t(ctypes.Structure):
 
 class stem_decode_args_t(ctypes.Structure):
     _fields_ = [
-        ("cache", ctypes.c_void_p), ("q", ctypes.c_void_p),  # cache: a stem_cache_t's address
+        ("cache", ctypes.POINTER(stem_cache_t)), ("q", ctypes.c_void_p),
         ("rows", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("budget", ctypes.c_void_p),
         ("R", ctypes.c_int32), ("Hq", ctypes.c_int32), ("kcap", ctypes.c_int32),
-        ("dtype", ctypes.c_int32), ("method", ctypes.c_void_p),  # a stem_method_t's address
+        ("dtype", ctypes.c_int32), ("method", ctypes.POINTER(stem_method_t)),
         ("sel_idx", ctypes.c_void_p), ("sel_cnt", ctypes.c_void_p), ("out", ctypes.c_void_p),
         ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p),
@@ -136,7 +136,8 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     M = ctypes.POINTER(stem_method_t)
-    L = ctypes.POINTER(ctypes.c_int64)
+    C, L = ctypes.POINTER(stem_cache_t), ctypes.POINTER(ctypes.c_int64)
+    A = ctypes.POINTER(stem_decode_args_t)
     sig = {
         "stem_prefill": (I, [P, P, P, I, I, I, I, I, I, F, F, I, P, P, P]),
         "stem_prefill_ex": (I, [ctypes.POINTER(stem_args_t), P]),
@@ -163,12 +164,12 @@ def _load() -> ctypes.CDLL:
         "stem_select_p_m": (I, [P, P, I, I, I, I, M, P, P, P, P, Z, P]),
         "stem_varlen_workspace_size_m": (Z, [I, ctypes.POINTER(ctypes.c_int32), I, I, I, I, M]),
         "stem_cache_page_bytes": (Z, [I, I, I]),
-        "stem_cache_append": (I, [P, P, P, I, I, L, P, P, P, P]),
-        "stem_cache_read": (I, [P, P, P, I, I, L, P, P, P, P]),
-        "stem_decode_workspace_size": (Z, [P, I, I, I]),
-        "stem_decode_select": (I, [P, P]),
-        "stem_decode_attn": (I, [P, P]),
-        "stem_decode": (I, [P, P]),
+        "stem_cache_append": (I, [C, P, P, I, I, L, P, P, P, P]),
+        "stem_cache_read": (I, [C, P, P, I, I, L, P, P, P, P]),
+        "stem_decode_workspace_size": (Z, [C, I, I, I]),
+        "stem_decode_select": (I, [A, P]),
+        "stem_decode_attn": (I, [A, P]),
+        "stem_decode": (I, [A, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

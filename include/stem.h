@@ -465,7 +465,7 @@ int stem_cache_read(const stem_cache_t* c, void* k, void* v, int dtype, int T,
  *   method                        share, metric, beta, clamp (the schedule is in budget, the V
  *                                 summary in the cache); score must be STEM_SCORE_POOLED
  *   workspace                     stem_decode_workspace_size bytes, 256-byte aligned; calls that may
- *                                 overlap on the device need one each
+ *                                 overlap on the device need one each; stem_decode_select needs none
  * All but the cache struct, method and sizes are read on the device: a captured graph may be replayed
  * with new lens, table and page contents.
  */

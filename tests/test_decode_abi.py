@@ -92,9 +92,6 @@ for name in ("stem_decode_select", "stem_decode_attn", "stem_decode"):
         "more rows than sequences": g(rows=None, R=4), "no sequences": g(cache(nseq=0)),
         "pages null": g(cache(pages=None)),
         "f32 UNSUPPORTED": g(dtype=1), "many rows UNSUPPORTED": g(R=65536),
-        "workspace null WORKSPACE": g(workspace=None),
-        "workspace small WORKSPACE": g(workspace_bytes=4096),
-        "workspace unaligned WORKSPACE": g(workspace=FAKE + 128),
         "no rows OK": g(R=0),
     }
     if name != "stem_decode_attn":
@@ -103,7 +100,10 @@ for name in ("stem_decode_select", "stem_decode_attn", "stem_decode"):
                   "clamp": g(m_metric=1, m_clamp=2), "score": g(m_score=2),
                   "score UNSUPPORTED": g(m_score=1)})
     if name != "stem_decode_select":
-        r.update({"out null": g(out=None), "out unaligned": g(out=FAKE + 8),
+        r.update({"workspace null WORKSPACE": g(workspace=None),
+                  "workspace small WORKSPACE": g(workspace_bytes=4096),
+                  "workspace unaligned WORKSPACE": g(workspace=FAKE + 128),
+                  "out null": g(out=None), "out unaligned": g(out=FAKE + 8),
                   "lse unaligned": g(lse=FAKE + 2)})
 print(json.dumps(out))
 """
@@ -131,7 +131,9 @@ def test_sizes():
     c = S.stem_cache_t(None, None, None, None, 100, 8, 128, 128, S.STEM_KV_Q4, 3, 1024, 0)
     L = S.lib()
     n = L.stem_decode_workspace_size(ctypes.byref(c), 2, 32, 50)
-    assert n >= 2 * 32 * 1024 * 8
+    # the parts of an item (its CTAs' numerators), lists of 50 blocks a kv head or, per head, 200
+    assert n > 2 * 8 * 200 * 8
+    assert L.stem_decode_workspace_size(ctypes.byref(c), 4, 32, 50) > n
     assert L.stem_decode_workspace_size(ctypes.byref(c), 0, 32, 50) == 0
     assert L.stem_decode_workspace_size(ctypes.byref(c), 2, 33, 50) == 0
     assert L.stem_decode_workspace_size(ctypes.byref(c), 2, 32, 1025) == 0
