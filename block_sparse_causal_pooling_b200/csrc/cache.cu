@@ -26,7 +26,13 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// Eight consecutive channels of one row as they are in memory, and as float32.
+__device__ __forceinline__ uint32_t bf16_bits(float x) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+__device__ __forceinline__ float bits_bf16(uint32_t b) { return __uint_as_float(b << 16); }
+
+// Eight consecutive channels of one row as they are in memory, as float32, and their largest
+// magnitude as the bits of a float32 (ordered like the numbers, with infinity and NaN on top).
 template <typename T>
 struct Raw;
 template <>
@@ -44,6 +50,11 @@ struct Raw<__nv_bfloat16> {
       x[2 * n + 1] = __uint_as_float(w[n] & 0xffff0000u);
     }
   }
+  __device__ __forceinline__ uint32_t largest() const {
+    constexpr uint32_t kMag = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & kMag, u.y & kMag), __vmaxu2(u.z & kMag, u.w & kMag));
+    return max(m << 16, m & 0xffff0000u);
+  }
 };
 template <>
 struct Raw<float> {
@@ -57,11 +68,15 @@ struct Raw<float> {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
+  __device__ __forceinline__ uint32_t largest() const {
+    float x[8];
+    get(x);
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+    return m;
+  }
 };
-__device__ __forceinline__ uint32_t bf16_bits(float x) {
-  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-__device__ __forceinline__ float bits_bf16(uint32_t b) { return __uint_as_float(b << 16); }
 
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   uint32_t w[4];
@@ -74,53 +89,71 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
 }
 
+// Eight codes of a row and their scale. A 4- or 8-bit code c is held as the bits of the float32
+// kMagic + c, kMagic = 1.5 * 2^23 + offset: adding kMagic rounds to an integer (ties to even), the
+// bits are kBits + c + offset, and subtracting kMagic gives c as a float32 again. A 16-bit code is
+// the bfloat16's bits.
+constexpr uint32_t kBits = 0x4b400000u;  // 1.5 * 2^23
+template <int FMT>
+struct Codes {
+  static constexpr float kMagic = 12582912.f + static_cast<float>(Kv<FMT, 128>::OFFSET);
+  uint32_t b[8];
+  uint32_t scale;  // bfloat16 bits
+
+  __device__ __forceinline__ float code(int e) const {
+    return FMT == STEM_KV_BF16 ? bits_bf16(b[e]) : __uint_as_float(b[e]) - kMagic;
+  }
+  __device__ __forceinline__ float value(int e) const {
+    return FMT == STEM_KV_BF16 ? code(e) : bits_bf16(scale) * code(e);  // exact (8 + 7 bits)
+  }
+};
+
 // Quantises the 8 channels of this thread; the group's other channels are in the 3 neighbouring
-// lanes (a quad works on one row). x becomes the values that the codes stand for; code[] holds
-// offset codes (bfloat16 bits for the 16-bit format), the return value the scale's bits.
+// lanes (a quad works on one row). Called by whole warps.
 //
 // The quotients are the correctly rounded ones without a division each (a division has a branch,
-// which would run the 8 of them one after another: 7 us a tile where this takes a fraction): with
-// r = 1/s correctly rounded, q0 = x r, e = x - q0 s (exact in an FMA) and q = q0 + e r is the
-// rounded x / s (Markstein's correction). Powers of two keep x and s away from the range's ends.
-// max|x| / Q is rounded once from the double product with 1/Q: 24 bits over 7 or 127 are never
-// nearer than 2^-32 to a float32 tie unless they are one.
-template <int FMT>
-__device__ __forceinline__ uint32_t quantise(float (&x)[8], uint32_t (&code)[8]) {
+// which would run the 8 of them one after another): with r near 1/s, q0 = x r, e = x - q0 s (exact
+// in an FMA) and q = q0 + e r is x / s but for 2^-46 of it before its rounding (Markstein's
+// correction), and the quotient of a float32 by the 8 bits of s is never nearer than 2^-34 to a
+// rounding border unless it is on one. The same holds for max|x| / Q. |x / s| <= Q 256/255 < Q + 1/2,
+// so that codes need no clamp, while s is a normal number. Rows that are not within 2^+-50, or
+// not finite, take the plain way.
+template <int FMT, typename T>
+__device__ __forceinline__ void quantise(const Raw<T>& raw, Codes<FMT>& c) {
+  float x[8];
+  raw.get(x);
   if constexpr (FMT == STEM_KV_BF16) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      code[e] = bf16_bits(x[e]);
-      x[e] = bits_bf16(code[e]);
-    }
-    return 0;
+    for (int e = 0; e < 8; ++e) c.b[e] = bf16_bits(x[e]);
+    c.scale = 0;
   } else {
-    using L = Kv<FMT, 128>;
-    constexpr float kTop = static_cast<float>(L::QMAX);
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
-    // magnitudes as integers: ordered like the numbers, with infinity and NaN on top
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    constexpr float kTop = static_cast<float>(Kv<FMT, 128>::QMAX), kInv = 1.f / kTop;
+    uint32_t top = raw.largest();
     top = max(top, __shfl_xor_sync(kFull, top, 1));
     top = max(top, __shfl_xor_sync(kFull, top, 2));
-    const bool finite = top < 0x7f800000u;
-    const float largest = static_cast<float>(static_cast<double>(__uint_as_float(top)) *
-                                             (1.0 / static_cast<double>(L::QMAX)));
-    const uint32_t sb = finite ? bf16_bits(largest) : 0x7fc0u;
-    const float s = bits_bf16(sb);
-    const float pow2 = s < 0x1p-60f ? 0x1p64f : s > 0x1p60f ? 0x1p-64f : 1.f;
-    const float ss = finite ? s * pow2 : 0.f;
-    const float r = s > 0.f && finite ? __frcp_rn(ss) : 0.f;
+    const float amax = __uint_as_float(top);
+    // (0, or 2^-50 .. 2^50 as bits)
+    if (__all_sync(kFull, top == 0 || top - 0x26800000u < 0x58800000u - 0x26800000u)) {
+      const float t0 = amax * kInv;
+      c.scale = bf16_bits(fmaf(fmaf(-t0, kTop, amax), kInv, t0));
+      const float s = bits_bf16(c.scale);
+      const float r = top == 0 ? 0.f : __frcp_rn(s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float y = finite ? x[e] * pow2 : 0.f;
-      const float q0 = y * r;
-      float q = fmaf(fmaf(-q0, ss, y), r, q0);
-      q = fminf(fmaxf(q, -kTop), kTop) + kMagic;
-      x[e] = s * (q - kMagic);  // exact (at most 8 + 7 bits); NaN for a group that is not finite
-      code[e] = __float_as_uint(q) - __float_as_uint(kMagic) + L::OFFSET;
+      for (int e = 0; e < 8; ++e) {
+        const float q0 = x[e] * r;
+        c.b[e] = __float_as_uint(fmaf(fmaf(-q0, s, x[e]), r, q0) + Codes<FMT>::kMagic);
+      }
+    } else {
+      const bool finite = top < 0x7f800000u;
+      c.scale = finite ? bf16_bits(__fdiv_rn(amax, kTop)) : 0x7fc0u;
+      const float s = bits_bf16(c.scale);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float q = 0.f;
+        if (finite && s > 0.f) q = fminf(fmaxf(__fdiv_rn(x[e], s), -kTop), kTop);
+        c.b[e] = __float_as_uint(q + Codes<FMT>::kMagic);
+      }
     }
-    return sb;
   }
 }
 
@@ -143,104 +176,135 @@ struct Place {
   }
 };
 
+// The WPG words of a lane's group are neighbours: moved at once.
+template <int N>
+__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)[4]) {
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_words(unsigned char* p, const uint32_t (&w)[4]) {
+  if constexpr (N == 4)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else if constexpr (N == 2)
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+}
+
+// sum of b[e] << shift, less what kBits adds: every code at its place in a word.
+__device__ __forceinline__ constexpr uint32_t magic_sum() { return 0u; }
+template <typename... S>
+__device__ __forceinline__ constexpr uint32_t magic_sum(int shift, S... rest) {
+  return (kBits << shift) + magic_sum(rest...);
+}
+
 template <int FMT>
-__device__ __forceinline__ void k_words(const uint32_t (&c)[8], uint32_t (&w)[4]) {
+__device__ __forceinline__ void k_words(const Codes<FMT>& c, uint32_t (&w)[4]) {
+  const uint32_t(&b)[8] = c.b;
   if constexpr (FMT == STEM_KV_BF16) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) w[n] = c[2 * n] | c[2 * n + 1] << 16;
+    for (int n = 0; n < 4; ++n) w[n] = b[2 * n] | b[2 * n + 1] << 16;
   } else if constexpr (FMT == STEM_KV_Q8) {
 #pragma unroll
     for (int n = 0; n < 2; ++n)
-      w[n] = c[4 * n] | c[4 * n + 2] << 8 | c[4 * n + 1] << 16 | c[4 * n + 3] << 24;
+      w[n] = b[4 * n] + (b[4 * n + 2] << 8) + (b[4 * n + 1] << 16) + (b[4 * n + 3] << 24) -
+             magic_sum(0, 8, 16, 24);
   } else {
-    w[0] = c[0] | c[2] << 4 | c[4] << 8 | c[6] << 12 | c[1] << 16 | c[3] << 20 | c[5] << 24 |
-           c[7] << 28;
+    w[0] = b[0] + (b[2] << 4) + (b[4] << 8) + (b[6] << 12) + (b[1] << 16) + (b[3] << 20) +
+           (b[5] << 24) + (b[7] << 28) - magic_sum(0, 4, 8, 12, 16, 20, 24, 28);
   }
 }
 template <int FMT>
-__device__ __forceinline__ void k_codes(const uint32_t (&w)[4], uint32_t (&c)[8]) {
+__device__ __forceinline__ void k_codes(const uint32_t (&w)[4], Codes<FMT>& c) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     if constexpr (FMT == STEM_KV_BF16)
-      c[e] = w[e / 2] >> (16 * (e % 2)) & 0xffffu;
+      c.b[e] = w[e / 2] >> (16 * (e % 2)) & 0xffffu;
     else if constexpr (FMT == STEM_KV_Q8)
-      c[e] = w[e / 4] >> (16 * (e % 2) + 8 * (e % 4 / 2)) & 0xffu;
+      c.b[e] = (w[e / 4] >> (16 * (e % 2) + 8 * (e % 4 / 2)) & 0xffu) | kBits;
     else
-      c[e] = w[0] >> (16 * (e % 2) + 4 * (e / 2)) & 0xfu;
+      c.b[e] = (w[0] >> (16 * (e % 2) + 4 * (e / 2)) & 0xfu) | kBits;
   }
 }
-// The 16-bit halves that one token has in the V words of 4 channels.
+// The 16-bit halves (in the low bits) that one token has in the V words of channels 4h .. 4h + 3.
 template <int FMT>
-__device__ __forceinline__ void v_halves(const uint32_t* c, uint32_t (&h)[4]) {
+__device__ __forceinline__ void v_halves(const Codes<FMT>& c, int h, uint32_t (&w)[4]) {
+  const uint32_t* b = c.b + 4 * h;
   if constexpr (FMT == STEM_KV_BF16) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) h[n] = c[n];
+    for (int n = 0; n < 4; ++n) w[n] = b[n];
   } else if constexpr (FMT == STEM_KV_Q8) {
-    h[0] = c[0] | c[1] << 8;
-    h[1] = c[2] | c[3] << 8;
+    w[0] = b[0] + (b[1] << 8) - magic_sum(0, 8);
+    w[1] = b[2] + (b[3] << 8) - magic_sum(0, 8);
   } else {
-    h[0] = c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12;
+    w[0] = b[0] + (b[1] << 4) + (b[2] << 8) + (b[3] << 12) - magic_sum(0, 4, 8, 12);
   }
 }
 template <int FMT>
-__device__ __forceinline__ void v_codes(const uint32_t (&h)[4], uint32_t* c) {
+__device__ __forceinline__ void v_codes(const uint32_t (&w)[4], int h, Codes<FMT>& c) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if constexpr (FMT == STEM_KV_BF16)
-      c[e] = h[e];
+      c.b[4 * h + e] = w[e];
     else if constexpr (FMT == STEM_KV_Q8)
-      c[e] = h[e / 2] >> (8 * (e % 2)) & 0xffu;
+      c.b[4 * h + e] = (w[e / 2] >> (8 * (e % 2)) & 0xffu) | kBits;
     else
-      c[e] = h[0] >> (4 * e) & 0xfu;
+      c.b[4 * h + e] = (w[0] >> (4 * e) & 0xfu) | kBits;
   }
 }
 
-template <int FMT>
-__device__ __forceinline__ void values(const uint32_t (&c)[8], uint32_t scale, float (&x)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if constexpr (FMT == STEM_KV_BF16)
-      x[e] = bits_bf16(c[e]);
-    else
-      x[e] = bits_bf16(scale) * static_cast<float>(static_cast<int>(c[e]) - Kv<FMT, 128>::OFFSET);
-  }
-}
-
-// K and V values of the pair's tokens y = 0, 1 from a tile in memory.
+// Scale bits of token 2 * pair + y in a tile: of its K group, or of its V group.
 template <int FMT, int D>
-__device__ __forceinline__ void read_pair(const unsigned char* tile, const Place<FMT, D>& at,
-                                          float (&xk)[2][8], float (&xv)[2][8]) {
+__device__ __forceinline__ uint16_t* scale_at(unsigned char* tile, const Place<FMT, D>& at, int y,
+                                              bool v) {
   using L = Kv<FMT, D>;
-  uint32_t vw[2][4];
+  return reinterpret_cast<uint16_t*>(tile + 2 * L::CODES + (2 * at.pair + y) * L::SCROW) +
+         (v ? L::NG : 0) + at.g;
+}
+
+// What a pair's tokens have in a tile, as it is in memory.
+template <int FMT, int D>
+struct Stored {
+  uint32_t k[2][4], v[2][4], sk[2], sv[2];
+
+  __device__ __forceinline__ void load(unsigned char* tile, const Place<FMT, D>& at) {
+    using L = Kv<FMT, D>;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int w = 0; w < L::WPG; ++w)
-      vw[h][w] = *reinterpret_cast<const uint32_t*>(tile + L::CODES + at.v(h, w));
-#pragma unroll
-  for (int y = 0; y < 2; ++y) {
-    uint32_t sk = 0, sv = 0;
-    if constexpr (FMT != STEM_KV_BF16) {
-      const unsigned char* row = tile + 2 * L::CODES + (2 * at.pair + y) * L::SCROW;
-      sk = *reinterpret_cast<const uint16_t*>(row + 2 * at.g);
-      sv = *reinterpret_cast<const uint16_t*>(row + 2 * (L::NG + at.g));
+    for (int y = 0; y < 2; ++y) {
+      load_words<L::WPG>(tile + at.k(y, 0), k[y]);
+      load_words<L::WPG>(tile + L::CODES + at.v(y, 0), v[y]);  // (of channels 4y .. 4y + 3)
+      if constexpr (FMT != STEM_KV_BF16) {
+        sk[y] = *scale_at(tile, at, y, false);
+        sv[y] = *scale_at(tile, at, y, true);
+      } else {
+        sk[y] = sv[y] = 0;
+      }
     }
-    uint32_t kw[4] = {0, 0, 0, 0}, c[8];
-#pragma unroll
-    for (int w = 0; w < L::WPG; ++w)
-      kw[w] = *reinterpret_cast<const uint32_t*>(tile + at.k(y, w));
-    k_codes<FMT>(kw, c);
-    values<FMT>(c, sk, xk[y]);
+  }
+  // K, or V, codes of token y of the pair
+  __device__ __forceinline__ void get_k(int y, Codes<FMT>& c) const {
+    c.scale = sk[y];
+    k_codes(k[y], c);
+  }
+  __device__ __forceinline__ void get_v(int y, Codes<FMT>& c) const {
+    c.scale = sv[y];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t hv[4];
+      uint32_t w[4];
 #pragma unroll
-      for (int w = 0; w < L::WPG; ++w) hv[w] = vw[h][w] >> (16 * y) & 0xffffu;
-      v_codes<FMT>(hv, c + 4 * h);
+      for (int n = 0; n < Kv<FMT, D>::WPG; ++n) w[n] = v[h][n] >> (16 * y) & 0xffffu;
+      v_codes(w, h, c);
     }
-    values<FMT>(c, sv, xv[y]);
   }
-}
+};
 
 struct Rows {
   const int32_t* pos;    // first token of each sequence's rows
@@ -264,9 +328,12 @@ __device__ __forceinline__ bool my_block(const KvCache& c, const Rows& r, int& p
 }
 
 constexpr int kThreads = 256;
+// CTAs an SM. Loads of one CTA hide behind the others' work: with 2 and the next tile's rows loaded
+// ahead a 128K prompt at 16 bits takes 377 us (written and read back), with 3 and none ahead 356.
+constexpr int kAppendCtas = 3;
 
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kThreads) append_kernel(KvCache c, Rows r, const T* k,
+__global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(KvCache c_, Rows r, const T* k,
                                                           const T* v) {
   using L = Kv<FMT, D>;
   constexpr int CH = D / 8;                    // chunks of a row
@@ -274,14 +341,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache c, Rows r, con
   int page, first, lo, hi;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
-  if (!my_block(c, r, page, first, lo, hi)) return;
+  if (!my_block(c_, r, page, first, lo, hi)) return;
   const int head = blockIdx.y, slot = threadIdx.x / (8 * CH);
   const int pair = threadIdx.x / CH % 8, chunk = threadIdx.x % CH;
   const Place<FMT, D> at(pair, chunk);
-  unsigned char* rec = c.at(page, head);
+  unsigned char* rec = c_.at(page, head);
   const int64_t base = static_cast<int64_t>(blockIdx.z) * r.s_seq +
                        static_cast<int64_t>(head) * r.s_head + chunk * 8;
-  const bool done = hi == c.block;  // the block is complete: all of its tokens are summarised
+  const bool done = hi == c_.block;  // the block is complete: all of its tokens are summarised
   float ksum[8] = {0, 0, 0, 0, 0, 0, 0, 0}, vacc = 0.f;
   const int n_end = (hi - 1) / kKvTile + 1;
   // tiles of a thread are n0, n0 + SLOTS, ..: an order that depends on token positions alone
@@ -301,94 +368,94 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache c, Rows r, con
       }
     }
   };
-  fetch(n);
   for (; n < n_end; n += SLOTS) {  // (a warp has one slot: n is uniform in it)
+    fetch(n);
     unsigned char* tile = rec + static_cast<int64_t>(n) * L::TILE_BYTES;
     const int t0 = n * kKvTile + 2 * pair;
-    bool fresh[2];
-    float xk[2][8], xv[2][8];
+    const bool fresh[2] = {t0 >= lo && t0 < hi, t0 + 1 >= lo && t0 + 1 < hi};
+    const bool any = __any_sync(kFull, fresh[0] || fresh[1]);
+    Codes<FMT> c[2];
+    // tokens that came with earlier calls are read back where the block is summarised
+    Stored<FMT, D> old;
+    if (done && !(fresh[0] && fresh[1])) old.load(tile, at);
+    __syncwarp();
+    // ---- K
+    if (any) {
+      uint32_t w[4];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      fresh[y] = t0 + y >= lo && t0 + y < hi;
-      rk[y].get(xk[y]);
-      rv[y].get(xv[y]);
+      for (int y = 0; y < 2; ++y) {
+        quantise(rk[y], c[y]);
+        if (fresh[y]) {
+          k_words(c[y], w);
+          store_words<L::WPG>(tile + at.k(y, 0), w);
+          if (FMT != STEM_KV_BF16 && at.q == 0)
+            *scale_at(tile, at, y, false) = static_cast<uint16_t>(c[y].scale);
+        }
+      }
     }
-    fetch(n + SLOTS);
-    if (__any_sync(kFull, fresh[0] || fresh[1])) {
+    if (done) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if (!fresh[y]) old.get_k(y, c[y]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          ksum[e] = FMT == STEM_KV_BF16 ? ksum[e] + c[y].code(e)
+                                        : fmaf(bits_bf16(c[y].scale), c[y].code(e), ksum[e]);
+      }
+    }
+    // ---- V
+    if (any) {
       uint32_t hv[2][2][4];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        uint32_t ck[8], cv[8], kw[4];
-        const uint32_t sk = quantise<FMT>(xk[y], ck), sv = quantise<FMT>(xv[y], cv);
-        v_halves<FMT>(cv, hv[y][0]);
-        v_halves<FMT>(cv + 4, hv[y][1]);
-        if (fresh[y]) {
-          k_words<FMT>(ck, kw);
-          if constexpr (FMT == STEM_KV_BF16) {
-            *reinterpret_cast<uint4*>(tile + at.k(y, 0)) = make_uint4(kw[0], kw[1], kw[2], kw[3]);
-          } else {
-#pragma unroll
-            for (int w = 0; w < L::WPG; ++w)
-              *reinterpret_cast<uint32_t*>(tile + at.k(y, w)) = kw[w];
-            if (at.q == 0) {
-              unsigned char* row = tile + 2 * L::CODES + (2 * pair + y) * L::SCROW;
-              *reinterpret_cast<uint16_t*>(row + 2 * at.g) = static_cast<uint16_t>(sk);
-              *reinterpret_cast<uint16_t*>(row + 2 * (L::NG + at.g)) = static_cast<uint16_t>(sv);
-            }
-          }
-        }
+        quantise(rv[y], c[y]);
+        v_halves(c[y], 0, hv[y][0]);
+        v_halves(c[y], 1, hv[y][1]);
+        if (FMT != STEM_KV_BF16 && fresh[y] && at.q == 0)
+          *scale_at(tile, at, y, true) = static_cast<uint16_t>(c[y].scale);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        unsigned char* dst = tile + L::CODES;
+        unsigned char* dst = tile + L::CODES + at.v(h, 0);
         if (fresh[0] && fresh[1]) {
-          uint32_t w4[4];
+          uint32_t w[4];
 #pragma unroll
-          for (int w = 0; w < L::WPG; ++w) w4[w] = hv[0][h][w] | hv[1][h][w] << 16;
-          if constexpr (FMT == STEM_KV_BF16) {
-            *reinterpret_cast<uint4*>(dst + at.v(h, 0)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-          } else {
-#pragma unroll
-            for (int w = 0; w < L::WPG; ++w)
-              *reinterpret_cast<uint32_t*>(dst + at.v(h, w)) = w4[w];
-          }
+          for (int i = 0; i < L::WPG; ++i) w[i] = hv[0][h][i] | hv[1][h][i] << 16;
+          store_words<L::WPG>(dst, w);
         } else {
           // a lone token writes its halves and leaves the other token's as they are
 #pragma unroll
           for (int y = 0; y < 2; ++y)
             if (fresh[y])
 #pragma unroll
-              for (int w = 0; w < L::WPG; ++w)
-                *reinterpret_cast<uint16_t*>(dst + at.v(h, w) + 2 * y) =
-                    static_cast<uint16_t>(hv[y][h][w]);
+              for (int i = 0; i < L::WPG; ++i)
+                *reinterpret_cast<uint16_t*>(dst + 4 * i + 2 * y) =
+                    static_cast<uint16_t>(hv[y][h][i]);
         }
       }
     }
     if (done) {
-      if (!(fresh[0] && fresh[1])) {  // tokens that came with earlier calls
-        float ok[2][8], ov[2][8];
-        read_pair<FMT, D>(tile, at, ok, ov);
+      float norm[2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-          if (!fresh[y])
+      for (int y = 0; y < 2; ++y) {
+        if (!fresh[y]) old.get_v(y, c[y]);
+        float sq = 0.f;  // of codes: a sum of integers below 2^24, exact
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xk[y][e] = ok[y][e], xv[y][e] = ov[y][e];
+        for (int e = 0; e < 8; ++e) sq = fmaf(c[y].code(e), c[y].code(e), sq);
+        if (FMT != STEM_KV_BF16) {
+          const float s = bits_bf16(c[y].scale);
+          sq *= s * s;
+        }
+        norm[y] = sq;
       }
       __syncwarp();
-      float sq[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ksum[e] += xk[0][e] + xk[1][e];
-        sq[0] = fmaf(xv[0][e], xv[0][e], sq[0]);
-        sq[1] = fmaf(xv[1][e], xv[1][e], sq[1]);
+      for (int d = 1; d < CH; d *= 2) {
+        norm[0] += __shfl_xor_sync(kFull, norm[0], d);
+        norm[1] += __shfl_xor_sync(kFull, norm[1], d);
       }
-#pragma unroll
-      for (int o = 1; o < CH; o *= 2) {
-        sq[0] += __shfl_xor_sync(kFull, sq[0], o);
-        sq[1] += __shfl_xor_sync(kFull, sq[1], o);
-      }
-      const float n0 = sqrtf(sq[0]), n1 = sqrtf(sq[1]);
-      if (c.vmax) {  // (NaN stays: a comparison with it is false)
+      const float n0 = sqrtf(norm[0]), n1 = sqrtf(norm[1]);
+      if (c_.vmax) {  // (NaN stays: a comparison with it is false)
         const float m = n0 > n1 || isnan(n0) ? n0 : n1;
         vacc = vacc > m || isnan(vacc) ? vacc : m;
       } else {
@@ -408,7 +475,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache c, Rows r, con
         make_float4(ksum[e], ksum[e + 1], ksum[e + 2], ksum[e + 3]);
   if (chunk == 0) vs[part] = vacc;
   __syncthreads();
-  const int64_t ph = static_cast<int64_t>(page) * c.Hkv + head;
+  const int64_t ph = static_cast<int64_t>(page) * c_.Hkv + head;
   if (threadIdx.x < D) {
     const int d = threadIdx.x;
     float s[P];
@@ -418,34 +485,34 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache c, Rows r, con
     for (int o = 1; o < P; o *= 2)
 #pragma unroll
       for (int i = 0; i < P; i += 2 * o) s[i] += s[i + o];
-    c.kbar[ph * D + d] = s[0] / static_cast<float>(c.block);
+    c_.kbar[ph * D + d] = s[0] / static_cast<float>(c_.block);
   } else if (threadIdx.x == D) {
     float s = vs[0];
     for (int i = 1; i < P; ++i) {
-      if (c.vmax)
+      if (c_.vmax)
         s = s > vs[i] || isnan(s) ? s : vs[i];
       else
         s += vs[i];
     }
-    c.vnorm[ph] = c.vmax ? s : s / static_cast<float>(c.block);
+    c_.vnorm[ph] = c_.vmax ? s : s / static_cast<float>(c_.block);
   }
 }
 
 // A CTA reads kReadTiles tiles, each thread its words of one tile at a time.
-constexpr int kReadTiles = 4;
+constexpr int kReadTiles = 2;
 
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(8 * (D / 8)) read_kernel(KvCache c, Rows r, T* k, T* v) {
+__global__ void __launch_bounds__(8 * (D / 8)) read_kernel(KvCache c_, Rows r, T* k, T* v) {
   using L = Kv<FMT, D>;
   constexpr int CH = D / 8;
   int page, first, lo, hi;
-  const int parts = c.block / (kReadTiles * kKvTile);
+  const int parts = c_.block / (kReadTiles * kKvTile);
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
-  if (!my_block(c, r, page, first, lo, hi, parts)) return;
+  if (!my_block(c_, r, page, first, lo, hi, parts)) return;
   const int head = blockIdx.y, pair = threadIdx.x / CH, chunk = threadIdx.x % CH;
   const Place<FMT, D> at(pair, chunk);
-  const unsigned char* rec = c.at(page, head);
+  unsigned char* rec = c_.at(page, head);
   const int64_t base = static_cast<int64_t>(blockIdx.z) * r.s_seq +
                        static_cast<int64_t>(head) * r.s_head + chunk * 8;
   const int n0 = blockIdx.x % parts * kReadTiles;
@@ -454,14 +521,23 @@ __global__ void __launch_bounds__(8 * (D / 8)) read_kernel(KvCache c, Rows r, T*
     const int t0 = (n0 + i) * kKvTile + 2 * pair;
     const bool live[2] = {t0 >= lo && t0 < hi, t0 + 1 >= lo && t0 + 1 < hi};
     if (!live[0] && !live[1]) continue;
-    float xk[2][8], xv[2][8];
-    read_pair<FMT, D>(rec + static_cast<int64_t>(n0 + i) * L::TILE_BYTES, at, xk, xv);
+    unsigned char* tile = rec + static_cast<int64_t>(n0 + i) * L::TILE_BYTES;
+    Stored<FMT, D> got;
+    got.load(tile, at);
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       if (!live[y]) continue;
       const int64_t o = base + static_cast<int64_t>(first + t0 + y) * r.s_tok;
-      store8(k + o, xk[y]);
-      store8(v + o, xv[y]);
+      Codes<FMT> c;
+      float x[8];
+      got.get_k(y, c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = c.value(e);
+      store8(k + o, x);
+      got.get_v(y, c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = c.value(e);
+      store8(v + o, x);
     }
   }
 }
