@@ -98,8 +98,8 @@ int cache_rows(bool write, const stem_cache_t* c, void* k, void* v, int dtype, i
 size_t workspace(const stem_cache_t* c, int R, int Hq, int kcap) {
   size_t most = kAlign;
   for (int share = 0; share < 2; ++share) {
-    const size_t n = decode_attn_bytes(c->format, c->D, c->Hkv, c->max_blocks, R, Hq, kcap,
-                                       share != 0);
+    const size_t n = decode_attn_bytes(c->format, c->D, c->block, c->Hkv, c->max_blocks, R, Hq,
+                                       kcap, share != 0);
     if (n > most) most = n;
   }
   return align_up(most);

@@ -41,7 +41,12 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kHeadTile = kDecodeHeads;
-constexpr int kMinEntries = 4;   // of a CTA, where fewer CTAs than fit then have work
+// Steps of a CTA below which an item is not split further: four a warp. (One row over 52 blocks of
+// 4 bits: 104 CTAs of 16 steps take 16.3 us, 208 of 8 steps 17.4, 416 of 4 steps 21.4.)
+#ifndef MS
+#define MS 8
+#endif
+constexpr int kMinSteps = MS;
 // Items in parts are joined by the CTA that brings the last part, which saves a launch, unless they
 // have more parts than this on average: then by a kernel of their own, with a CTA for each head.
 constexpr int kDirect = 16;
@@ -142,6 +147,9 @@ struct Args {
   DecodeLists lists;
   int items;  // a row, a kv head and up to 8 of its query heads each
   int ctas;
+  // CTAs of an item, of `chunk` entries or a little less each; 0: there are more items, or longer
+  // ones, than CTAs run at once, and the entries of all items are spread evenly over the CTAs
+  int per_item, chunk;
   __nv_bfloat16* out;
   float* lse;
   // Parts of items, two slots a CTA (its first item, and its last one): [slot][8] statistics (max in
@@ -234,6 +242,30 @@ struct Spread {
   __device__ __forceinline__ int cta_of(int entry) const {
     const int b = more * (each + 1);
     return entry < b ? entry / (each + 1) : more + (entry - b) / each;
+  }
+};
+
+// Parts of an item that has CTAs of its own.
+__device__ __forceinline__ int parts_of(const Args& a, int entries) {
+  return (entries + a.chunk - 1) / a.chunk;
+}
+
+// The parts of an item of n entries, the first of which has number e_item: their number, and the
+// slots they are in (slot0 + first, then slot0 + 2, slot0 + 4, ..).
+struct Parts {
+  int n, slot0, first;
+  __device__ __forceinline__ Parts(const Args& a, int total, int item, int e_item, int entries) {
+    if (a.per_item) {
+      n = parts_of(a, entries);
+      slot0 = 2 * item * a.per_item;
+      first = 0;
+    } else {
+      const Spread spread(total, a.ctas);
+      const int c0 = spread.cta_of(e_item);
+      n = spread.cta_of(e_item + entries - 1) - c0 + 1;
+      slot0 = 2 * c0;
+      first = spread.first(c0) == e_item ? 0 : 1;  // the item is the first one of all its other CTAs
+    }
   }
 };
 
@@ -374,7 +406,22 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
   const int G = a.r.Hq / a.c.Hkv;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
-  find_begin<C::WARPS>(a, &s_begin, s_sum);
+  int item, entry, e_at, e_end, total = 0;
+  if (a.per_item) {
+    item = blockIdx.x / a.per_item;
+    const int n = a.lists.count[list_of(a, item)], parts = parts_of(a, n);
+    const int part = blockIdx.x % a.per_item;
+    e_at = entry = n * part / max(parts, 1);
+    e_end = part < parts ? n * (part + 1) / parts : entry;
+  } else {
+    find_begin<C::WARPS>(a, &s_begin, s_sum);
+    total = s_begin.total;
+    item = s_begin.item, entry = s_begin.entry;
+    e_at = Spread(total, a.ctas).first(blockIdx.x);
+    e_end = Spread(total, a.ctas).first(blockIdx.x + 1);
+    if (!a.direct && blockIdx.x == 0 && tid == 0) a.start[a.items] = total;
+  }
+  const int e_first = e_at;
   // rows that keep nothing
   for (int n = blockIdx.x; n < a.items; n += gridDim.x) {
     if (a.lists.count[list_of(a, n)] != 0) continue;
@@ -384,10 +431,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
       a.out[head0 * D + i] = __float2bfloat16_rn(0.f);
     if (tid < nh && a.lse) a.lse[head0 + tid] = -INFINITY;
   }
-  const Spread spread(s_begin.total, a.ctas);
-  if (!a.direct && blockIdx.x == 0 && tid == 0) a.start[a.items] = s_begin.total;
-  const int e_first = spread.first(blockIdx.x), e_end = spread.first(blockIdx.x + 1);
-  int item = s_begin.item, entry = s_begin.entry, e_at = e_first;
 
   // this CTA's part of one item after the other
   for (; e_at < e_end; ++item, entry = 0) {
@@ -923,16 +966,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
   }
   // ---- of an item in parts, the CTA that brings the last one joins them
   if (!whole && a.direct) {
-    const int c0 = spread.cta_of(e_item), parts = spread.cta_of(e_item + n_item - 1) - c0 + 1;
+    const Parts p(a, total, item, e_item, n_item);
     __threadfence();
     __syncthreads();
-    if (tid == 0) s_last = atomicAdd(&a.lists.arrived[item], 1) == parts - 1;
+    if (tid == 0) s_last = atomicAdd(&a.lists.arrived[item], 1) == p.n - 1;
     __syncthreads();
     if (s_last) {
       __threadfence();  // (the other CTAs' parts are visible)
-      // the item is the first one of all its CTAs but, perhaps, c0
-      join_parts<D, C::WARPS>(a, head0, nh, parts, reinterpret_cast<float4*>(smem), 2 * c0,
-                              spread.first(c0) == e_item ? 0 : 1);
+      join_parts<D, C::WARPS>(a, head0, nh, p.n, reinterpret_cast<float4*>(smem), p.slot0, p.first);
     }
   } else if (!a.direct && entry == 0 && tid == 0) {
     a.start[item] = e_item;
@@ -957,11 +998,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   cudaTriggerProgrammaticLaunchCompletion();
   const int n = a.lists.count[list_of(a, item)];
   if (n == 0) return;
-  const Spread spread(a.start[a.items], a.ctas);
-  const int e0 = a.start[item], c0 = spread.cta_of(e0), parts = spread.cta_of(e0 + n - 1) - c0 + 1;
+  const Parts p(a, a.per_item ? 0 : a.start[a.items], item, a.per_item ? 0 : a.start[item], n);
+  const int parts = p.n;
   if (parts == 1) return;  // (its CTA has written the output)
-  const int first = spread.first(c0) == e0 ? 0 : 1;  // the item is its first CTA's first or last
-  auto slot = [&](int s) { return 2 * (c0 + s) + (s == 0 ? first : 0); };
+  auto slot = [&](int s) { return p.slot0 + 2 * s + (s == 0 ? p.first : 0); };
   float m = -INFINITY;
   for (int s = tid; s < parts; s += kJoinThreads) m = fmaxf(m, a.stat[slot(s) * kHeadTile + h].x);
   for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
@@ -1006,11 +1046,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
 
 // Sizes of a call, and where its arrays are in the workspace.
 struct Sizes {
-  int tiles_h, most, ctas;
+  int tiles_h, most, ctas, per_item, chunk;
   int64_t items, lists;
   size_t list, count, arrived, start, stat, part, total;
 };
-Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap, bool share) {
+Sizes sizes_of(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq, int kcap, bool share) {
   Sizes s;
   const int G = Hq / Hkv;
   s.tiles_h = (G + kHeadTile - 1) / kHeadTile;
@@ -1020,13 +1060,16 @@ Sizes sizes_of(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kc
   s.most = share ? kcap
                  : static_cast<int>(std::min<int64_t>(
                        static_cast<int64_t>(std::min(G, kHeadTile)) * kcap, max_blocks));
-  // as many CTAs as run at once, so that each gets the same number of blocks; fewer where that
-  // would be less than kMinEntries each
   const int per_sm = format == STEM_KV_Q4 ? Cfg<STEM_KV_Q4, 128>::CTAS
                      : format == STEM_KV_Q8 ? Cfg<STEM_KV_Q8, 128>::CTAS
                                             : Cfg<STEM_KV_BF16, 128>::CTAS;
-  s.ctas = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(sm_count()) * per_sm,
-                                              (s.items * s.most + kMinEntries - 1) / kMinEntries));
+  const int steps = block / (format == STEM_KV_BF16 ? Cfg<STEM_KV_BF16, 128>::STEP
+                                                    : Cfg<STEM_KV_Q4, 128>::STEP);
+  const int64_t at_once = static_cast<int64_t>(sm_count()) * per_sm;
+  s.chunk = std::max(1, kMinSteps / steps);
+  s.per_item = (s.most + s.chunk - 1) / s.chunk;
+  s.ctas = static_cast<int>(std::min<int64_t>(s.items * s.per_item, at_once));
+  if (s.items * s.per_item > at_once) s.per_item = 0;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1071,7 +1114,7 @@ cudaError_t launch(const Args& a, bool planned, cudaStream_t st) {
 
 DecodeLists decode_lists(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
                          unsigned char* ws) {
-  const Sizes s = sizes_of(format, D, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
+  const Sizes s = sizes_of(format, D, c.block, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
   DecodeLists l;
   l.list = reinterpret_cast<Entry*>(ws + s.list);
   l.count = reinterpret_cast<int32_t*>(ws + s.count);
@@ -1084,7 +1127,7 @@ DecodeLists decode_lists(const KvCache& c, int format, int D, const DecodeRows& 
 cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
                                bool planned, void* out, float* lse, unsigned char* ws,
                                cudaStream_t st) {
-  const Sizes s = sizes_of(format, D, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
+  const Sizes s = sizes_of(format, D, c.block, c.Hkv, c.max_blocks, r.R, r.Hq, r.kcap, share);
   Args a;
   a.c = c;
   a.r = r;
@@ -1092,6 +1135,8 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   a.lists = decode_lists(c, format, D, r, share, ws);
   a.items = static_cast<int>(s.items);
   a.ctas = s.ctas;
+  a.per_item = s.per_item;
+  a.chunk = s.chunk;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.direct = s.ctas <= kDirect * s.items;
@@ -1112,9 +1157,9 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   }
 }
 
-size_t decode_attn_bytes(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap,
-                         bool share) {
-  return sizes_of(format, D, Hkv, max_blocks, R, Hq, kcap, share).total;
+size_t decode_attn_bytes(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq,
+                         int kcap, bool share) {
+  return sizes_of(format, D, block, Hkv, max_blocks, R, Hq, kcap, share).total;
 }
 
 }  // namespace stem

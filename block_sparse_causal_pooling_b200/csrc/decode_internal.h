@@ -62,7 +62,7 @@ DecodeLists decode_lists(const KvCache& c, int format, int D, const DecodeRows& 
 cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const DecodeRows& r, bool share,
                                bool planned, void* out, float* lse, unsigned char* ws,
                                cudaStream_t st);
-size_t decode_attn_bytes(int format, int D, int Hkv, int max_blocks, int R, int Hq, int kcap,
-                         bool share);
+size_t decode_attn_bytes(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq,
+                         int kcap, bool share);
 
 }  // namespace stem

@@ -121,6 +121,23 @@ __device__ void pick(const double* key, int last, int want, Team<T>& s) {
     s.sync();
     return;
   }
+  // Few candidates: each counts those that come before it.
+  constexpr int kFew = T == 32 ? 64 : 128;
+  if (last <= kFew) {
+    s.sync();
+    for (int j = 1 + tid; j < last; j += T) {
+      const double x = key[j];
+      int before = 0;
+#pragma unroll 4
+      for (int n = 1; n < last; ++n) {
+        const double y = key[n];
+        before += y > x || (y == x && n < j);
+      }
+      if (before < want) atomicOr(&s.kept[j / 32], 1u << (j % 32));
+    }
+    s.sync();
+    return;
+  }
   double lo = INFINITY, hi = -INFINITY;  // of the finite keys
   for (int j = 1 + tid; j < last; j += T) {
     const double x = key[j];
