@@ -41,12 +41,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kHeadTile = kDecodeHeads;
-// Steps of a CTA below which an item is not split further: four a warp. (One row over 52 blocks of
-// 4 bits: 104 CTAs of 16 steps take 16.3 us, 208 of 8 steps 17.4, 416 of 4 steps 21.4.)
-#ifndef MS
-#define MS 8
-#endif
-constexpr int kMinSteps = MS;
+// Steps of a CTA below which an item is not split further: two a warp. (A short context, 10 blocks:
+// 12.7 us with 8 steps a CTA, 13.6 with 16; one row over 52 blocks: 14.8 and 14.7.)
+constexpr int kMinSteps = 8;
 // Items in parts are joined by the CTA that brings the last part, which saves a launch, unless they
 // have more parts than this on average: then by a kernel of their own, with a CTA for each head.
 constexpr int kDirect = 16;
