@@ -143,18 +143,18 @@ struct Args {
   bool share;
   DecodeLists lists;
   int items;  // a row, a kv head and up to 8 of its query heads each
-  int ctas;
-  // CTAs of an item, of `chunk` entries or a little less each; 0: there are more items, or longer
-  // ones, than CTAs run at once, and the entries of all items are spread evenly over the CTAs
-  int per_item, chunk;
+  // A CTA has one part of one item: `chunk` entries, or a little less. With per_item CTAs for each item
+  // the chunk is fixed; where they would not all run at once (per_item 0), it follows from the number
+  // of entries that there are, so that about at_once CTAs have the work of all.
+  int per_item, chunk, at_once;
   __nv_bfloat16* out;
   float* lse;
-  // Parts of items, two slots a CTA (its first item, and its last one): [slot][8] statistics (max in
-  // log2 units, sum for the output, sum for lse) and [slot][8][D] numerators.
+  // Parts of items, a slot for each CTA: [slot][8] statistics (max in log2 units, sum for the output,
+  // sum for lse) and [slot][8][D] numerators.
   float4* stat;
   float* part;
-  bool direct;    // the CTA that brings an item's last part joins them
-  int32_t* start; // [items]: number of the item's first entry; [items]: total (where not direct)
+  bool direct;     // the CTA that brings an item's last part joins them
+  int32_t* start;  // [items]: the item's first CTA; [items]: the chunk (where neither is fixed)
 };
 
 // ------------------------------------------------------------------ the lists
@@ -224,98 +224,66 @@ __device__ __forceinline__ int list_of(const Args& a, int item) {
   return a.share ? item / a.lists.tiles_h : item;
 }
 
-// Entries are numbered over the items in order and spread evenly over N = min(ctas, total) CTAs: the
-// first total % N of them take one more than the others.
-struct Spread {
-  int total, each, more;
-  __device__ __forceinline__ Spread(int total_, int ctas) : total(total_) {
-    const int n = max(min(ctas, total), 1);
-    each = total / n;
-    more = total - each * n;
-  }
-  __device__ __forceinline__ int first(int cta) const {  // (total for the CTAs without entries)
-    return min(each * cta + min(cta, more), total);
-  }
-  __device__ __forceinline__ int cta_of(int entry) const {
-    const int b = more * (each + 1);
-    return entry < b ? entry / (each + 1) : more + (entry - b) / each;
-  }
-};
-
-// Parts of an item that has CTAs of its own.
-__device__ __forceinline__ int parts_of(const Args& a, int entries) {
-  return (entries + a.chunk - 1) / a.chunk;
-}
-
-// The parts of an item of n entries, the first of which has number e_item: their number, and the
-// slots they are in (slot0 + first, then slot0 + 2, slot0 + 4, ..).
-struct Parts {
-  int n, slot0, first;
-  __device__ __forceinline__ Parts(const Args& a, int total, int item, int e_item, int entries) {
-    if (a.per_item) {
-      n = parts_of(a, entries);
-      slot0 = 2 * item * a.per_item;
-      first = 0;
-    } else {
-      const Spread spread(total, a.ctas);
-      const int c0 = spread.cta_of(e_item);
-      n = spread.cta_of(e_item + entries - 1) - c0 + 1;
-      slot0 = 2 * c0;
-      first = spread.first(c0) == e_item ? 0 : 1;  // the item is the first one of all its other CTAs
-    }
-  }
-};
-
-// The item that a CTA's first entry is in, and the entry's number there. The CTA sums the counts of
-// all items (every CTA the same ones, from L2).
-struct Begin {
-  int total, item, entry;
+// The item that this CTA has a part of (items: none), the item's first CTA, and the chunk. Every CTA
+// sums the counts of all items (from L2) for the chunk, then the parts for its place among them.
+struct Place {
+  int item, first, chunk;
 };
 template <int WARPS>
-__device__ __forceinline__ void find_begin(const Args& a, Begin* sh, int* wsum) {
-  const int tid = threadIdx.x, run = (a.items + WARPS * 32 - 1) / (WARPS * 32);
-  const int i0 = min(tid * run, a.items), i1 = min(i0 + run, a.items);
-  int n = 0;
-  for (int i = i0; i < i1; ++i) n += a.lists.count[list_of(a, i)];
+__device__ __forceinline__ int cta_scan(int n, int* wsum, int& total) {  // sums before this thread's
   int s = n;
   for (int o = 1; o < 32; o *= 2) {
     const int y = __shfl_up_sync(kFull, s, o);
-    if (tid % 32 >= o) s += y;
+    if (threadIdx.x % 32 >= o) s += y;
   }
-  if (tid % 32 == 31) wsum[tid / 32] = s;
   __syncthreads();
-  int total = 0;
+  if (threadIdx.x % 32 == 31) wsum[threadIdx.x / 32] = s;
+  __syncthreads();
+  total = 0;
   for (int w = 0; w < WARPS; ++w) {
-    if (w < tid / 32) s += wsum[w];
+    if (w < static_cast<int>(threadIdx.x) / 32) s += wsum[w];
     total += wsum[w];
   }
-  s -= n;
-  const int first = Spread(total, a.ctas).first(blockIdx.x);
-  if (first >= s && first < s + n) {
+  return s - n;
+}
+template <int WARPS>
+__device__ __forceinline__ void find_place(const Args& a, Place* sh, int* wsum) {
+  const int run = (a.items + WARPS * 32 - 1) / (WARPS * 32);
+  const int i0 = min(static_cast<int>(threadIdx.x) * run, a.items), i1 = min(i0 + run, a.items);
+  int n = 0, total, parts = 0;
+  for (int i = i0; i < i1; ++i) n += a.lists.count[list_of(a, i)];
+  cta_scan<WARPS>(n, wsum, total);
+  // half as much again as an even share: fewer items are cut, and the CTAs that come free take the
+  // rest. (32 ragged rows of per-head lists at 16 bits: 101 us with 1.5 or 2 even shares, 111 with
+  // 1.25; 64 rows at 4 bits: 94 with 1.5, 96 with 2, 98 with 1.25.)
+  const int chunk = max(a.chunk, (total / 2 * 3 + a.at_once - 1) / a.at_once);
+  for (int i = i0; i < i1; ++i) parts += (a.lists.count[list_of(a, i)] + chunk - 1) / chunk;
+  int s = cta_scan<WARPS>(parts, wsum, total);
+  const int cta = blockIdx.x;
+  if (cta >= s && cta < s + parts) {
     int i = i0;
     for (;; ++i) {
-      const int c = a.lists.count[list_of(a, i)];
-      if (first < s + c) break;
+      const int c = (a.lists.count[list_of(a, i)] + chunk - 1) / chunk;
+      if (cta < s + c) break;
       s += c;
     }
-    *sh = Begin{total, i, first - s};
-  } else if (first >= total && tid == 0) {
-    *sh = Begin{total, 0, 0};  // no entries here
+    *sh = Place{i, s, chunk};
+  } else if (cta >= total && threadIdx.x == 0) {
+    *sh = Place{a.items, 0, chunk};
   }
   __syncthreads();
 }
 
 // Joins parts of an item, once they are all there: a warp for each head, a lane for 4 channels (at
-// 64 channels the warp's halves take parts in turn). Part 0 is in slot slot0 + slot_first, part s in
-// slot0 + 2 s; st holds kJoinStaged statistics.
+// 64 channels the warp's halves take parts in turn). Part s is in slot slot0 + s; st holds kJoinStaged
+// statistics.
 constexpr int kJoinStaged = 512;
 
 // (Not inlined, and its loops mostly not unrolled: it runs once or twice in a CTA, and fetching
 // straight-line code for the first time costs more than running it.)
 template <int D, int WARPS>
 __device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, int parts,
-                                        float4* st, int slot0, int slot_first) {
-  auto slot = [&](int s) { return slot0 + 2 * s + (s == 0 ? slot_first : 0); };
+                                        float4* st, int slot0) {
   constexpr int kLanes = D / 4, kHalves = 32 / kLanes, kAtOnce = 8;
   const int lane = threadIdx.x % 32, c = lane % kLanes, half = lane / kLanes;
   const int most = kJoinStaged / nh;  // parts staged at a time
@@ -329,7 +297,7 @@ __device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, in
       __syncthreads();
 #pragma unroll 1
       for (int i = threadIdx.x; i < n * nh; i += WARPS * 32)
-        st[i] = __ldcg(&a.stat[slot(s0 + i / nh) * kHeadTile + i % nh]);
+        st[i] = __ldcg(&a.stat[(slot0 + s0 + i / nh) * kHeadTile + i % nh]);
       __syncthreads();
       float top = m;
 #pragma unroll 1
@@ -354,7 +322,7 @@ __device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, in
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {  // (past the end: the last part again, with weight 0)
           const int e = min(i0 + i * kHalves, n - 1);
-          p[i] = __ldcg(src + static_cast<int64_t>(slot(s0 + e)) * (kHeadTile * D / 4));
+          p[i] = __ldcg(src + static_cast<int64_t>(slot0 + s0 + e) * (kHeadTile * D / 4));
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
@@ -393,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
   constexpr bool kQuant = C::Q;
   constexpr int NG = L::NG, TPS = C::TPS;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ Begin s_begin;
+  __shared__ Place s_place;
   __shared__ int s_sum[C::WARPS];
   __shared__ bool s_last;
   __shared__ Entry ent[kStaged];
@@ -403,22 +371,18 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
   const int G = a.r.Hq / a.c.Hkv;
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
-  int item, entry, e_at, e_end, total = 0;
+  int item, first, chunk = a.chunk;  // the item of this CTA, and its first CTA
   if (a.per_item) {
     item = blockIdx.x / a.per_item;
-    const int n = a.lists.count[list_of(a, item)], parts = parts_of(a, n);
-    const int part = blockIdx.x % a.per_item;
-    e_at = entry = n * part / max(parts, 1);
-    e_end = part < parts ? n * (part + 1) / parts : entry;
+    first = item * a.per_item;
   } else {
-    find_begin<C::WARPS>(a, &s_begin, s_sum);
-    total = s_begin.total;
-    item = s_begin.item, entry = s_begin.entry;
-    e_at = Spread(total, a.ctas).first(blockIdx.x);
-    e_end = Spread(total, a.ctas).first(blockIdx.x + 1);
-    if (!a.direct && blockIdx.x == 0 && tid == 0) a.start[a.items] = total;
+    find_place<C::WARPS>(a, &s_place, s_sum);
+    item = s_place.item, first = s_place.first, chunk = s_place.chunk;
+    if (!a.direct && tid == 0) {
+      if (blockIdx.x == 0) a.start[a.items] = chunk;
+      if (item < a.items && static_cast<int>(blockIdx.x) == first) a.start[item] = first;
+    }
   }
-  const int e_first = e_at;
   // rows that keep nothing
   for (int n = blockIdx.x; n < a.items; n += gridDim.x) {
     if (a.lists.count[list_of(a, n)] != 0) continue;
@@ -429,15 +393,13 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
     if (tid < nh && a.lse) a.lse[head0 + tid] = -INFINITY;
   }
 
-  // this CTA's part of one item after the other
-  for (; e_at < e_end; ++item, entry = 0) {
-  const int n_item = a.lists.count[list_of(a, item)];
-  const int n_ent = min(n_item - entry, e_end - e_at);
-  if (n_ent <= 0) continue;
-  const bool whole = n_ent == n_item;
-  const int slot = 2 * blockIdx.x + (e_at == e_first ? 0 : 1);
-  const int e_item = e_at - entry;  // number of the item's first entry
-  e_at += n_ent;
+  if (item >= a.items) return;
+  const int n_item = a.lists.count[list_of(a, item)], parts = (n_item + chunk - 1) / chunk;
+  const int part = static_cast<int>(blockIdx.x) - first;
+  if (part >= parts) return;
+  const int entry = n_item * part / parts, n_ent = n_item * (part + 1) / parts - entry;
+  const bool whole = parts == 1;
+  const int slot = blockIdx.x;
   const Entry* list = a.lists.list + static_cast<int64_t>(list_of(a, item)) * a.lists.most + entry;
   const int row = item / (a.c.Hkv * a.lists.tiles_h), kv = item / a.lists.tiles_h % a.c.Hkv;
   const int h0 = item % a.lists.tiles_h * kHeadTile;
@@ -963,19 +925,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
   }
   // ---- of an item in parts, the CTA that brings the last one joins them
   if (!whole && a.direct) {
-    const Parts p(a, total, item, e_item, n_item);
     __threadfence();
     __syncthreads();
-    if (tid == 0) s_last = atomicAdd(&a.lists.arrived[item], 1) == p.n - 1;
+    if (tid == 0) s_last = atomicAdd(&a.lists.arrived[item], 1) == parts - 1;
     __syncthreads();
     if (s_last) {
       __threadfence();  // (the other CTAs' parts are visible)
-      join_parts<D, C::WARPS>(a, head0, nh, p.n, reinterpret_cast<float4*>(smem), p.slot0, p.first);
+      join_parts<D, C::WARPS>(a, head0, nh, parts, reinterpret_cast<float4*>(smem), first);
     }
-  } else if (!a.direct && entry == 0 && tid == 0) {
-    a.start[item] = e_item;
-  }
-  __syncthreads();  // (the results in shared memory have been read)
   }
 }
 
@@ -986,7 +943,7 @@ constexpr int kJoinThreads = 512;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   constexpr int kGroups = kJoinThreads / D, kJoinWarps = kJoinThreads / 32;
-  extern __shared__ float weight[];  // ctas
+  extern __shared__ float weight[];  // [most]
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps], s_o[kGroups][D];
   const int row = blockIdx.y, head = blockIdx.x, tid = threadIdx.x;
   const int G = a.r.Hq / a.c.Hkv, h = head % G % kHeadTile;
@@ -995,12 +952,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   cudaTriggerProgrammaticLaunchCompletion();
   const int n = a.lists.count[list_of(a, item)];
   if (n == 0) return;
-  const Parts p(a, a.per_item ? 0 : a.start[a.items], item, a.per_item ? 0 : a.start[item], n);
-  const int parts = p.n;
+  const int chunk = a.per_item ? a.chunk : a.start[a.items], parts = (n + chunk - 1) / chunk;
   if (parts == 1) return;  // (its CTA has written the output)
-  auto slot = [&](int s) { return p.slot0 + 2 * s + (s == 0 ? p.first : 0); };
+  const int slot0 = a.per_item ? item * a.per_item : a.start[item];
   float m = -INFINITY;
-  for (int s = tid; s < parts; s += kJoinThreads) m = fmaxf(m, a.stat[slot(s) * kHeadTile + h].x);
+  for (int s = tid; s < parts; s += kJoinThreads) m = fmaxf(m, a.stat[(slot0 + s) * kHeadTile + h].x);
   for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
   if (tid % 32 == 0) s_m[tid / 32] = m;
   __syncthreads();
@@ -1009,7 +965,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f, lx = 0.f;
   for (int s = tid; s < parts; s += kJoinThreads) {
-    const float4 st = a.stat[slot(s) * kHeadTile + h];
+    const float4 st = a.stat[(slot0 + s) * kHeadTile + h];
     const float f = ex2(st.x - base);
     weight[s] = f;
     l = fmaf(f, st.y, l);
@@ -1026,7 +982,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   float x = 0.f;
 #pragma unroll 8
   for (int s = grp; s < parts; s += kGroups)
-    x = fmaf(weight[s], part[static_cast<int64_t>(slot(s)) * kHeadTile * D], x);
+    x = fmaf(weight[s], part[static_cast<int64_t>(slot0 + s) * kHeadTile * D], x);
   s_o[grp][d] = x;
   __syncthreads();
   if (grp == 0) {
@@ -1043,7 +999,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
 
 // Sizes of a call, and where its arrays are in the workspace.
 struct Sizes {
-  int tiles_h, most, ctas, per_item, chunk;
+  int tiles_h, most, ctas, per_item, chunk, at_once;
   int64_t items, lists;
   size_t list, count, arrived, start, stat, part, total;
 };
@@ -1062,11 +1018,16 @@ Sizes sizes_of(int format, int D, int block, int Hkv, int max_blocks, int R, int
                                             : Cfg<STEM_KV_BF16, 128>::CTAS;
   const int steps = block / (format == STEM_KV_BF16 ? Cfg<STEM_KV_BF16, 128>::STEP
                                                     : Cfg<STEM_KV_Q4, 128>::STEP);
-  const int64_t at_once = static_cast<int64_t>(sm_count()) * per_sm;
+  s.at_once = sm_count() * per_sm;
   s.chunk = std::max(1, kMinSteps / steps);
   s.per_item = (s.most + s.chunk - 1) / s.chunk;
-  s.ctas = static_cast<int>(std::min<int64_t>(s.items * s.per_item, at_once));
-  if (s.items * s.per_item > at_once) s.per_item = 0;
+  int64_t ctas = s.items * s.per_item;
+  if (ctas > s.at_once) {
+    // a chunk that is an at_once-th of the entries, or more, leaves at most this many parts
+    ctas = std::min<int64_t>(ctas, s.items + s.at_once);
+    s.per_item = 0;
+  }
+  s.ctas = static_cast<int>(ctas);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1075,7 +1036,7 @@ Sizes sizes_of(int format, int D, int block, int Hkv, int max_blocks, int R, int
   };
   s.list = take(sizeof(Entry) * static_cast<size_t>(s.lists) * s.most);
   s.count = take(sizeof(int32_t) * static_cast<size_t>(s.lists));
-  const size_t slots = 2 * static_cast<size_t>(s.ctas);
+  const size_t slots = static_cast<size_t>(s.ctas);
   s.arrived = take(sizeof(int32_t) * static_cast<size_t>(s.items));
   s.start = take(sizeof(int32_t) * static_cast<size_t>(s.items + 1));
   s.stat = take(sizeof(float4) * slots * kHeadTile);
@@ -1085,7 +1046,7 @@ Sizes sizes_of(int format, int D, int block, int Hkv, int max_blocks, int R, int
 }
 
 template <int FMT, int D>
-cudaError_t launch(const Args& a, bool planned, cudaStream_t st) {
+cudaError_t launch(const Args& a, int ctas, bool planned, cudaStream_t st) {
   using C = Cfg<FMT, D>;
   static_assert(C::RING >= kHeadTile * D * 4 && C::WARPS * C::RING >= kJoinStaged * 16,
                 "the rings hold the warps' results, then the parts' statistics, at the end");
@@ -1101,10 +1062,10 @@ cudaError_t launch(const Args& a, bool planned, cudaStream_t st) {
   e = cudaFuncSetAttribute(attn_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  e = launch_after(attn_kernel<FMT, D>, dim3(a.ctas), C::THREADS, bytes, 1, st, a);
+  e = launch_after(attn_kernel<FMT, D>, dim3(ctas), C::THREADS, bytes, 1, st, a);
   if (e != cudaSuccess || a.direct) return e;
-  return launch_after(join_kernel<D>, dim3(a.r.Hq, a.r.R), kJoinThreads, sizeof(float) * a.ctas, 1,
-                      st, a);
+  return launch_after(join_kernel<D>, dim3(a.r.Hq, a.r.R), kJoinThreads,
+                      sizeof(float) * a.lists.most, 1, st, a);
 }
 
 }  // namespace
@@ -1131,26 +1092,26 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   a.share = share;
   a.lists = decode_lists(c, format, D, r, share, ws);
   a.items = static_cast<int>(s.items);
-  a.ctas = s.ctas;
   a.per_item = s.per_item;
   a.chunk = s.chunk;
+  a.at_once = s.at_once;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
-  a.direct = s.ctas <= kDirect * s.items;
+  a.direct = std::min(s.ctas, s.at_once) <= kDirect * s.items;
   a.start = reinterpret_cast<int32_t*>(ws + s.start);
   a.stat = reinterpret_cast<float4*>(ws + s.stat);
   a.part = reinterpret_cast<float*>(ws + s.part);
   if (D == 128) {
     switch (format) {
-      case STEM_KV_BF16: return launch<STEM_KV_BF16, 128>(a, planned, st);
-      case STEM_KV_Q8: return launch<STEM_KV_Q8, 128>(a, planned, st);
-      default: return launch<STEM_KV_Q4, 128>(a, planned, st);
+      case STEM_KV_BF16: return launch<STEM_KV_BF16, 128>(a, s.ctas, planned, st);
+      case STEM_KV_Q8: return launch<STEM_KV_Q8, 128>(a, s.ctas, planned, st);
+      default: return launch<STEM_KV_Q4, 128>(a, s.ctas, planned, st);
     }
   }
   switch (format) {
-    case STEM_KV_BF16: return launch<STEM_KV_BF16, 64>(a, planned, st);
-    case STEM_KV_Q8: return launch<STEM_KV_Q8, 64>(a, planned, st);
-    default: return launch<STEM_KV_Q4, 64>(a, planned, st);
+    case STEM_KV_BF16: return launch<STEM_KV_BF16, 64>(a, s.ctas, planned, st);
+    case STEM_KV_Q8: return launch<STEM_KV_Q8, 64>(a, s.ctas, planned, st);
+    default: return launch<STEM_KV_Q4, 64>(a, s.ctas, planned, st);
   }
 }
 
