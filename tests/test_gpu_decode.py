@@ -327,6 +327,55 @@ def test_select_ties_and_odd_summaries(share):
                 assert int(cnt[0, h]) == k
 
 
+@pytest.mark.parametrize("share", ["head", "group"])
+@pytest.mark.parametrize("metric", ["product", "additive"])
+@pytest.mark.parametrize("nb,G,D", [(40, 1, 64), (200, 4, 128), (700, 8, 64), (1500, 11, 128)])
+def test_select_among_blocks_that_nearly_tie(share, metric, nb, G, D):
+    """Summaries that differ in their last digits: keys closer than float32 arithmetic can tell apart,
+    for all rows or for some, decided as double precision decides."""
+    g = torch.Generator().manual_seed(nb)
+    table, pages = make_table([nb], nb, spare=0)
+    gpu, _ = pair(pages, 1, D, 64, "q4", table)
+    for spread, some in ((1e-6, 1.0), (3e-5, 1.0), (1e-6, 0.3)):
+        kb, vn = fill_summaries(gpu, g)
+        near = torch.rand(pages, 1, 1, generator=g) < some
+        kb = torch.where(near, kb[:1] + spread * kb, kb)
+        vn = torch.where(near[..., 0], vn[:1] * (1 + spread * torch.randn(pages, 1, generator=g)), vn)
+        gpu.kbar.copy_(kb)
+        gpu.vnorm.copy_(vn)
+        q = rows(g, 4, G, D)
+        lens = [nb * 64, nb * 64 - 100, nb * 40, 64 * 9 + 1]
+        for rho in (0.05, 0.5):
+            m = S.make_method("exp", rho_min=rho, tau=2.0, k_min=3, share=share, metric=metric, beta=0.2)
+            budget, kcap = S.stem_decode_budget(nb, m, DEV)
+            idx, cnt = S.stem_decode_select(gpu, q.to(DEV), i32(lens), budget, kcap, m,
+                                            rows=i32([0] * 4))
+            check_select(gpu, q, [0] * 4, lens, budget.tolist(), kb, vn, table, share, metric,
+                         float(np.float32(0.2)), True, idx, cnt, kcap)
+
+
+def test_select_with_infinite_summaries():
+    """Infinite scores: first where they are +infinity, last where -infinity or not a number."""
+    g = torch.Generator().manual_seed(21)
+    D, nb = 64, 90
+    table, pages = make_table([nb], nb, spare=0)
+    gpu, _ = pair(pages, 1, D, 64, "q8", table)
+    kb, vn = fill_summaries(gpu, g)
+    q = rows(g, 1, 2, D)
+    kb[5, 0, 3], kb[17, 0, 3], kb[40, 0, 3] = float("inf"), float("-inf"), float("nan")
+    vn[30], vn[31] = float("inf"), 0.0
+    gpu.kbar.copy_(kb)
+    gpu.vnorm.copy_(vn)
+    for k in (3, 4, 9, 60, 87, 88):
+        m = S.make_method("exp", rho_min=1.0, tau=1.0)
+        budget = torch.full((nb,), k, dtype=torch.int32, device=DEV)
+        idx, cnt = S.stem_decode_select(gpu, q.to(DEV), i32([nb * 64]), budget, k, m)
+        pg = table[0, :nb - 1]
+        lists, _ = ref.select(q[0], kb[pg, 0], vn[pg, 0], nb - 1, k, "head", "product")
+        for h in range(2):
+            assert idx[0, h].tolist() == lists[h] and int(cnt[0, h]) == k
+
+
 def test_select_reports_bad_rows_budgets_and_pages():
     D, block, nb = 64, 64, 8
     table = np.arange(2 * nb, dtype=np.int32).reshape(2, nb)
