@@ -5,14 +5,14 @@
 // heads of its kv head (2 to 8 flops a byte at 16 bits), so HBM bounds the kernel and the tensor
 // pipe has room to spare. It uses mma.sync.m16n8k16 with tokens (for V: channels) as the 16 rows
 // and 8 query heads as the 8 columns: tcgen05's 128-row tiles would need the expanded codes in
-// shared memory, four times the bytes that were read, to feed a unit that is idle 90% of the time.
+// shared memory, four times the bytes of 4-bit codes, for 8 useful columns or rows.
 //
 // Codes of 4 and 8 bits go to the MMA without a conversion: a masked word holds a pair of fp16
 // subnormals code * 2^-24 (times 16 for the upper nibble of a byte, undone in q or at the end).
-//   K: sum_d q_d (c_d - off) over a 32-channel group is one short chain of MMAs whose accumulator
-//      starts at -off * sum_d q_d; the group's scale multiplies its result (4 FMA a tile and group).
-//      q is scaled by a power of two per head so that its largest entry is in [2^14, 2^15): bf16's 8
-//      significant bits survive in fp16.
+//   K: sum_d q_d c_d over a 32-channel group is one short chain of MMAs; the group's scale multiplies
+//      its result (4 FMA a tile and group). What the offset adds over all groups, sum_y s_ty off_yh with
+//      off_yh = -offset * sum_d q_d, is one more MMA, of the scales. q is scaled by a power of two per
+//      head so that its largest entry is in [2^14, 2^15): bf16's 8 significant bits survive in fp16.
 //   V: the scale goes to the weight: a_th = p_th s_t f rounded once to fp16, with f a power of two
 //      that follows the largest scale seen (like the running maximum of the softmax), so that no
 //      range of scales overflows or underflows. sum_t a_th (c_td - off) = sum a c - off * sum a; the
@@ -27,6 +27,11 @@
 // A warp streams whole tiles (16 tokens of K and V, contiguous in the page) through a ring of its own
 // in shared memory with cp.async: no barrier between warps until the end. Softmax statistics and
 // sums are float32. Warps, then CTAs of one (row, kv head), are joined by (max, sum, numerator).
+//
+// Measured (B200; 16 sequences, 32 heads on 8 kv heads of 128, every block; device time in a graph),
+// at 4K, 8K, 16K and 32K tokens: 16 bits 56, 95, 173 and 329 us, 8 bits 42, 65, 111 and 205 us, 4 bits
+// 43, 57, 90 and 157 us; at 32K 6.5, 5.6 and 3.9 TB/s (a copy reaches 6.47). A line through the four
+// has a slope of 6.9, 6.1 and 4.6 TB/s and starts at 17, 18 and 25 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -66,7 +71,7 @@ struct Cfg {
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
   // CTAs an SM: as many as registers allow at 4 and 8 bits, and the rings at 16.
   static constexpr int CTAS = FMT == STEM_KV_Q4 ? 4 : FMT == STEM_KV_Q8 ? 3 : 2;
-  static constexpr int STEP = kKvTile * TPS;                                      // tokens
+  static constexpr int STEP = kKvTile * TPS;  // tokens
   static constexpr int STEP_BYTES = TPS * L::TILE_BYTES;
   static constexpr int RING = STAGES * STEP_BYTES;  // a warp's
 };
@@ -162,7 +167,8 @@ struct Args {
 constexpr int kPlanThreads = 128;
 
 // Turns the kept blocks of each (row, kv head) or item into a list of entries: the page of each
-// block and the heads that keep it. One CTA per list.
+// block and the heads that keep it. One CTA per list. (After a selection of the same call the lists are
+// there already.)
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a) {
   extern __shared__ uint32_t mask[];  // per-head lists: a byte of head bits for each block
   __shared__ uint32_t wbuf[kPlanThreads / 32];
@@ -253,10 +259,7 @@ __device__ __forceinline__ void find_place(const Args& a, Place* sh, int* wsum) 
   int n = 0, total, parts = 0;
   for (int i = i0; i < i1; ++i) n += a.lists.count[list_of(a, i)];
   cta_scan<WARPS>(n, wsum, total);
-  // half as much again as an even share: fewer items are cut, and the CTAs that come free take the
-  // rest. (32 ragged rows of per-head lists at 16 bits: 101 us with 1.5 or 2 even shares, 111 with
-  // 1.25; 64 rows at 4 bits: 94 with 1.5, 96 with 2, 98 with 1.25.)
-  const int chunk = max(a.chunk, (total / 2 * 3 + a.at_once - 1) / a.at_once);
+  const int chunk = part_entries(total, a.at_once, a.chunk);
   for (int i = i0; i < i1; ++i) parts += (a.lists.count[list_of(a, i)] + chunk - 1) / chunk;
   int s = cta_scan<WARPS>(parts, wsum, total);
   const int cta = blockIdx.x;
@@ -505,308 +508,308 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
     vf0 = vf1 = 1.f;
     vlim0 = vlim1 = -1;
     for (int e0 = 0; e0 < n_ent; e0 += kStaged) {
-    __syncthreads();
-    const int n_now = min(n_ent - e0, kStaged);
-    for (int n = tid; n < n_now; n += C::THREADS) ent[n] = list[e0 + n];
-    __syncthreads();
-    // Warp w takes steps [u0, u1) of the staged entries, one after the other: two walkers, one
-    // that fetches and one that computes, look at an entry when they come to it.
-    const int units = n_now << spb_log, per_entry = 1 << spb_log;
-    const int u0 = units * warp / C::WARPS, u1 = units * (warp + 1) / C::WARPS;
-    auto tokens = [&](const Entry& e) -> int {  // of an entry; 0 or less: nothing to do
-      return e.what >> 16 & heads ? len - static_cast<int>(e.what & 0xffffu) * a.c.block : 0;
-    };
-    int fu = u0, ftok = 0;
-    const unsigned char* fsrc = nullptr;
-    auto fetch = [&](int stage) {
-      if (fu < u1) {
-        if (fu == u0 || (fu & (per_entry - 1)) == 0) {
-          const Entry e = ent[fu >> spb_log];
-          const int skip = fu & (per_entry - 1);
-          ftok = tokens(e) - skip * C::STEP;
-          fsrc = head_pages + e.page * page_bytes + skip * C::STEP_BYTES;
-        }
-        if (ftok > 0) {
-          unsigned char* dst = ring + stage * C::STEP_BYTES + lane * 16;
-#pragma unroll
-          for (int n = 0; n < C::STEP_BYTES / 512; ++n) cp16(dst + n * 512, fsrc + n * 512);
-          if (C::STEP_BYTES % 512 != 0 && lane < C::STEP_BYTES % 512 / 16)
-            cp16(dst + C::STEP_BYTES / 512 * 512, fsrc + C::STEP_BYTES / 512 * 512);
-        }
-        ftok -= C::STEP;
-        fsrc += C::STEP_BYTES;
-        ++fu;
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int n = 0; n < C::STAGES - 1; ++n) fetch(n);
-    int stage = 0, valid = 0;
-    uint32_t hb = 0;
-    for (int u = u0; u < u1; ++u) {
-      // the next step to fetch takes the stage that the step before this one has left
-      fetch(stage == 0 ? C::STAGES - 1 : stage - 1);
-      cp_wait<C::STAGES - 1>();
-      __syncwarp();
-      if (u == u0 || (u & (per_entry - 1)) == 0) {
-        const Entry e = ent[u >> spb_log];
-        valid = tokens(e) - (u & (per_entry - 1)) * C::STEP;
-        hb = e.what >> 16 & heads;
-      }
-      if (valid > 0) {
-        const unsigned char* step = ring + stage * C::STEP_BYTES;
-        // ---- logits: rows are tokens g and g + 8 of a tile, columns heads 2t and 2t + 1
-        float z[TPS][4];
-        uint32_t sv[TPS][2][2];  // V scales of tokens g, g + 8: two groups a word
-        if constexpr (!kQuant) {
-#pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            const uint4 ka = *reinterpret_cast<const uint4*>(step + L::word(0, y, 0, lane));
-            const uint4 kb = *reinterpret_cast<const uint4*>(step + L::word(1, y, 0, lane));
-            if (y == 0)
-              mma_bf16_new(z[0], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
-            else
-              mma_bf16(z[0], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
-            mma_bf16(z[0], ka.z, kb.z, ka.w, kb.w, qf[y][2], qf[y][3]);
+      __syncthreads();
+      const int n_now = min(n_ent - e0, kStaged);
+      for (int n = tid; n < n_now; n += C::THREADS) ent[n] = list[e0 + n];
+      __syncthreads();
+      // Warp w takes steps [u0, u1) of the staged entries, one after the other: two walkers, one
+      // that fetches and one that computes, look at an entry when they come to it.
+      const int units = n_now << spb_log, per_entry = 1 << spb_log;
+      const int u0 = units * warp / C::WARPS, u1 = units * (warp + 1) / C::WARPS;
+      auto tokens = [&](const Entry& e) -> int {  // of an entry; 0 or less: nothing to do
+        return e.what >> 16 & heads ? len - static_cast<int>(e.what & 0xffffu) * a.c.block : 0;
+      };
+      int fu = u0, ftok = 0;
+      const unsigned char* fsrc = nullptr;
+      auto fetch = [&](int stage) {
+        if (fu < u1) {
+          if (fu == u0 || (fu & (per_entry - 1)) == 0) {
+            const Entry e = ent[fu >> spb_log];
+            const int skip = fu & (per_entry - 1);
+            ftok = tokens(e) - skip * C::STEP;
+            fsrc = head_pages + e.page * page_bytes + skip * C::STEP_BYTES;
           }
-        } else {
-          uint32_t kw[TPS][2][NG * L::WPG], sk[TPS][2][2];
+          if (ftok > 0) {
+            unsigned char* dst = ring + stage * C::STEP_BYTES + lane * 16;
 #pragma unroll
-          for (int i = 0; i < TPS; ++i) {
-            const unsigned char* tile = step + i * L::TILE_BYTES;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const unsigned char* s = tile + 2 * L::CODES + (g + 8 * r) * L::SCROW;
-              if constexpr (NG == 4) {
-                const uint4 x = *reinterpret_cast<const uint4*>(s);
-                sk[i][r][0] = x.x, sk[i][r][1] = x.y, sv[i][r][0] = x.z, sv[i][r][1] = x.w;
-              } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(s);
-                sk[i][r][0] = x.x, sv[i][r][0] = x.y;
-                sk[i][r][1] = sv[i][r][1] = 0;
-              }
-            }
-            const uint32_t s0 = NG == 4 && (t & 1) ? sk[i][0][1] : sk[i][0][0];
-            const uint32_t s1 = NG == 4 && (t & 1) ? sk[i][1][1] : sk[i][1][0];
-            mma_bf16_new(z[i], s0, s1, s0, s1, ob0, ob1);
-#pragma unroll
-            for (int p = 0; p < L::PIECES; ++p) {
-              const uint4 x = *reinterpret_cast<const uint4*>(tile + p * 512 + lane * 16);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                kw[i][(p * 4 + n) / (NG * L::WPG)][(p * 4 + n) % (NG * L::WPG)] = w[n];
-            }
+            for (int n = 0; n < C::STEP_BYTES / 512; ++n) cp16(dst + n * 512, fsrc + n * 512);
+            if (C::STEP_BYTES % 512 != 0 && lane < C::STEP_BYTES % 512 / 16)
+              cp16(dst + C::STEP_BYTES / 512 * 512, fsrc + C::STEP_BYTES / 512 * 512);
           }
+          ftok -= C::STEP;
+          fsrc += C::STEP_BYTES;
+          ++fu;
+        }
+        cp_commit();
+      };
 #pragma unroll
-          for (int y = 0; y < NG; ++y) {
+      for (int n = 0; n < C::STAGES - 1; ++n) fetch(n);
+      int stage = 0, valid = 0;
+      uint32_t hb = 0;
+      for (int u = u0; u < u1; ++u) {
+        // the next step to fetch takes the stage that the step before this one has left
+        fetch(stage == 0 ? C::STAGES - 1 : stage - 1);
+        cp_wait<C::STAGES - 1>();
+        __syncwarp();
+        if (u == u0 || (u & (per_entry - 1)) == 0) {
+          const Entry e = ent[u >> spb_log];
+          valid = tokens(e) - (u & (per_entry - 1)) * C::STEP;
+          hb = e.what >> 16 & heads;
+        }
+        if (valid > 0) {
+          const unsigned char* step = ring + stage * C::STEP_BYTES;
+          // ---- logits: rows are tokens g and g + 8 of a tile, columns heads 2t and 2t + 1
+          float z[TPS][4];
+          uint32_t sv[TPS][2][2];  // V scales of tokens g, g + 8: two groups a word
+          if constexpr (!kQuant) {
+#pragma unroll
+            for (int y = 0; y < NG; ++y) {
+              const uint4 ka = *reinterpret_cast<const uint4*>(step + L::word(0, y, 0, lane));
+              const uint4 kb = *reinterpret_cast<const uint4*>(step + L::word(1, y, 0, lane));
+              if (y == 0)
+                mma_bf16_new(z[0], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
+              else
+                mma_bf16(z[0], ka.x, kb.x, ka.y, kb.y, qf[y][0], qf[y][1]);
+              mma_bf16(z[0], ka.z, kb.z, ka.w, kb.w, qf[y][2], qf[y][3]);
+            }
+          } else {
+            uint32_t kw[TPS][2][NG * L::WPG], sk[TPS][2][2];
 #pragma unroll
             for (int i = 0; i < TPS; ++i) {
-              float d[4];
-              if constexpr (FMT == STEM_KV_Q4) {
-                const uint32_t a0 = kw[i][0][y], a1 = kw[i][1][y];
-                mma_f16_new(d, a0 & 0x000f000fu, a1 & 0x000f000fu, a0 & 0x00f000f0u,
-                            a1 & 0x00f000f0u, qf[y][0], qf[y][1]);
-                mma_f16(d, a0 >> 8 & 0x000f000fu, a1 >> 8 & 0x000f000fu, a0 >> 8 & 0x00f000f0u,
-                        a1 >> 8 & 0x00f000f0u, qf[y][2], qf[y][3]);
-              } else {
-                const uint32_t a0 = kw[i][0][2 * y], a1 = kw[i][1][2 * y];
-                const uint32_t b0 = kw[i][0][2 * y + 1], b1 = kw[i][1][2 * y + 1];
-                mma_f16_new(d, a0 & 0x00ff00ffu, a1 & 0x00ff00ffu, a0 >> 8 & 0x00ff00ffu,
-                            a1 >> 8 & 0x00ff00ffu, qf[y][0], qf[y][1]);
-                mma_f16(d, b0 & 0x00ff00ffu, b1 & 0x00ff00ffu, b0 >> 8 & 0x00ff00ffu,
-                        b1 >> 8 & 0x00ff00ffu, qf[y][2], qf[y][3]);
+              const unsigned char* tile = step + i * L::TILE_BYTES;
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const unsigned char* s = tile + 2 * L::CODES + (g + 8 * r) * L::SCROW;
+                if constexpr (NG == 4) {
+                  const uint4 x = *reinterpret_cast<const uint4*>(s);
+                  sk[i][r][0] = x.x, sk[i][r][1] = x.y, sv[i][r][0] = x.z, sv[i][r][1] = x.w;
+                } else {
+                  const uint2 x = *reinterpret_cast<const uint2*>(s);
+                  sk[i][r][0] = x.x, sv[i][r][0] = x.y;
+                  sk[i][r][1] = sv[i][r][1] = 0;
+                }
               }
-              const float s0 = y & 1 ? high16(sk[i][0][y / 2]) : low16(sk[i][0][y / 2]);
-              const float s1 = y & 1 ? high16(sk[i][1][y / 2]) : low16(sk[i][1][y / 2]);
-              z[i][0] = fmaf(s0, d[0], z[i][0]);
-              z[i][1] = fmaf(s0, d[1], z[i][1]);
-              z[i][2] = fmaf(s1, d[2], z[i][2]);
-              z[i][3] = fmaf(s1, d[3], z[i][3]);
+              const uint32_t s0 = NG == 4 && (t & 1) ? sk[i][0][1] : sk[i][0][0];
+              const uint32_t s1 = NG == 4 && (t & 1) ? sk[i][1][1] : sk[i][1][0];
+              mma_bf16_new(z[i], s0, s1, s0, s1, ob0, ob1);
+#pragma unroll
+              for (int p = 0; p < L::PIECES; ++p) {
+                const uint4 x = *reinterpret_cast<const uint4*>(tile + p * 512 + lane * 16);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                  kw[i][(p * 4 + n) / (NG * L::WPG)][(p * 4 + n) % (NG * L::WPG)] = w[n];
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < NG; ++y) {
+#pragma unroll
+              for (int i = 0; i < TPS; ++i) {
+                float d[4];
+                if constexpr (FMT == STEM_KV_Q4) {
+                  const uint32_t a0 = kw[i][0][y], a1 = kw[i][1][y];
+                  mma_f16_new(d, a0 & 0x000f000fu, a1 & 0x000f000fu, a0 & 0x00f000f0u,
+                              a1 & 0x00f000f0u, qf[y][0], qf[y][1]);
+                  mma_f16(d, a0 >> 8 & 0x000f000fu, a1 >> 8 & 0x000f000fu, a0 >> 8 & 0x00f000f0u,
+                          a1 >> 8 & 0x00f000f0u, qf[y][2], qf[y][3]);
+                } else {
+                  const uint32_t a0 = kw[i][0][2 * y], a1 = kw[i][1][2 * y];
+                  const uint32_t b0 = kw[i][0][2 * y + 1], b1 = kw[i][1][2 * y + 1];
+                  mma_f16_new(d, a0 & 0x00ff00ffu, a1 & 0x00ff00ffu, a0 >> 8 & 0x00ff00ffu,
+                              a1 >> 8 & 0x00ff00ffu, qf[y][0], qf[y][1]);
+                  mma_f16(d, b0 & 0x00ff00ffu, b1 & 0x00ff00ffu, b0 >> 8 & 0x00ff00ffu,
+                          b1 >> 8 & 0x00ff00ffu, qf[y][2], qf[y][3]);
+                }
+                const float s0 = y & 1 ? high16(sk[i][0][y / 2]) : low16(sk[i][0][y / 2]);
+                const float s1 = y & 1 ? high16(sk[i][1][y / 2]) : low16(sk[i][1][y / 2]);
+                z[i][0] = fmaf(s0, d[0], z[i][0]);
+                z[i][1] = fmaf(s0, d[1], z[i][1]);
+                z[i][2] = fmaf(s1, d[2], z[i][2]);
+                z[i][3] = fmaf(s1, d[3], z[i][3]);
+              }
             }
           }
-        }
-        // ---- tokens past the row's length and heads that do not keep the block: weight 0, and
-        // scale 0, whatever their bytes hold
-        bool on0 = true, on1 = true;
-        if (valid < C::STEP || hb != 0xffu) {
-          on0 = hb >> (2 * t) & 1;
-          on1 = hb >> (2 * t + 1) & 1;
-#pragma unroll
-          for (int i = 0; i < TPS; ++i)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const bool in = i * kKvTile + 8 * r + g < valid;
-              if (!(in && on0)) z[i][2 * r] = -INFINITY;
-              if (!(in && on1)) z[i][2 * r + 1] = -INFINITY;
-              if (kQuant && !in) sv[i][r][0] = sv[i][r][1] = 0;
-            }
-        }
-        // ---- running maximum and scale: exact only when a logit or a scale leaves its slack
-        float n0 = fmaxf(z[0][0], z[0][2]), n1 = fmaxf(z[0][1], z[0][3]);
-        bool move = false;
-        if constexpr (kQuant) {
-          n0 = fmaxf(n0, fmaxf(z[1][0], z[1][2]));
-          n1 = fmaxf(n1, fmaxf(z[1][1], z[1][3]));
-          uint32_t top = __vmaxu2(__vmaxu2(sv[0][0][0], sv[0][1][0]),
-                                  __vmaxu2(sv[1][0][0], sv[1][1][0]));
-          if constexpr (NG == 4)
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(sv[0][0][1], sv[0][1][1]),
-                                         __vmaxu2(sv[1][0][1], sv[1][1][1])));
-          const int most = static_cast<int>(max(top & 0xffffu, top >> 16));
-          move = (on0 && most > vlim0) || (on1 && most > vlim1);
-        }
-        move |= n0 > lim0 || n1 > lim1;
-        if (__any_sync(kFull, move)) {
-          n0 *= qs0;
-          n1 *= qs1;
-#pragma unroll
-          for (int o = 4; o < 32; o *= 2) {
-            n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, o));
-            n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, o));
-          }
-          n0 = fmaxf(n0, m0);
-          n1 = fmaxf(n1, m1);
-          const float a0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
-          const float a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-          m0 = n0;
-          m1 = n1;
-          lim0 = (n0 + kSlack) * (1.f / qs0);
-          lim1 = (n1 + kSlack) * (1.f / qs1);
-          l0 *= a0;
-          l1 *= a1;
-          if constexpr (!kQuant) x0 *= a0, x1 *= a1;
-          float c0 = a0, c1 = a1;
-          if constexpr (kQuant) {
-            uint32_t top = 0;  // largest finite scale: bf16 bits order like the numbers
+          // ---- tokens past the row's length and heads that do not keep the block: weight 0, and
+          // scale 0, whatever their bytes hold
+          bool on0 = true, on1 = true;
+          if (valid < C::STEP || hb != 0xffu) {
+            on0 = hb >> (2 * t) & 1;
+            on1 = hb >> (2 * t + 1) & 1;
 #pragma unroll
             for (int i = 0; i < TPS; ++i)
 #pragma unroll
-              for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int w = 0; w < NG / 2; ++w) {
-                  const uint32_t lo = sv[i][r][w] & 0xffffu, hi = sv[i][r][w] >> 16;
-                  top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                }
-            top = __reduce_max_sync(kFull, top);
-            const uint32_t ex = top >> 7;  // biased exponent
-            const float f = __uint_as_float(min(254u + kScaleSet - ex, 245u) << 23);
-            const int lim = static_cast<int>((ex + kScaleSlack + 1) << 7) - 1;
-            if (on0 && static_cast<int>(top) > vlim0) {
-              if (vlim0 >= 0) c0 *= f / vf0;
-              vf0 = f;
-              vlim0 = lim;
-            }
-            if (on1 && static_cast<int>(top) > vlim1) {
-              if (vlim1 >= 0) c1 *= f / vf1;
-              vf1 = f;
-              vlim1 = lim;
-            }
+              for (int r = 0; r < 2; ++r) {
+                const bool in = i * kKvTile + 8 * r + g < valid;
+                if (!(in && on0)) z[i][2 * r] = -INFINITY;
+                if (!(in && on1)) z[i][2 * r + 1] = -INFINITY;
+                if (kQuant && !in) sv[i][r][0] = sv[i][r][1] = 0;
+              }
           }
-#pragma unroll
-          for (int n = 0; n < 2 * NG; ++n) {
-            acc[n][0] *= c0;
-            acc[n][1] *= c1;
-            acc[n][2] *= c0;
-            acc[n][3] *= c1;
+          // ---- running maximum and scale: exact only when a logit or a scale leaves its slack
+          float n0 = fmaxf(z[0][0], z[0][2]), n1 = fmaxf(z[0][1], z[0][3]);
+          bool move = false;
+          if constexpr (kQuant) {
+            n0 = fmaxf(n0, fmaxf(z[1][0], z[1][2]));
+            n1 = fmaxf(n1, fmaxf(z[1][1], z[1][3]));
+            uint32_t top = __vmaxu2(__vmaxu2(sv[0][0][0], sv[0][1][0]),
+                                    __vmaxu2(sv[1][0][0], sv[1][1][0]));
+            if constexpr (NG == 4)
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(sv[0][0][1], sv[0][1][1]),
+                                           __vmaxu2(sv[1][0][1], sv[1][1][1])));
+            const int most = static_cast<int>(max(top & 0xffffu, top >> 16));
+            move = (on0 && most > vlim0) || (on1 && most > vlim1);
           }
-          asum[0] *= c0;
-          asum[1] *= c1;
-          asum[2] *= c0;
-          asum[3] *= c1;
-        }
-        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-        float p[TPS][4];
+          move |= n0 > lim0 || n1 > lim1;
+          if (__any_sync(kFull, move)) {
+            n0 *= qs0;
+            n1 *= qs1;
 #pragma unroll
-        for (int i = 0; i < TPS; ++i) {
-          p[i][0] = ex2(fmaf(z[i][0], qs0, -b0));
-          p[i][1] = ex2(fmaf(z[i][1], qs1, -b1));
-          p[i][2] = ex2(fmaf(z[i][2], qs0, -b0));
-          p[i][3] = ex2(fmaf(z[i][3], qs1, -b1));
-        }
-        // ---- O^T += V^T P: rows are channels, P^T is P transposed in registers
-        if constexpr (!kQuant) {
-          const unsigned char* vt = step + L::CODES;
-          x0 += p[0][0] + p[0][2];
-          x1 += p[0][1] + p[0][3];
-          const uint32_t pa = pack_bf16(p[0][0], p[0][1]), pb = pack_bf16(p[0][2], p[0][3]);
-          l0 += low16(pa) + low16(pb);
-          l1 += high16(pa) + high16(pb);
-          const uint32_t w0 = transpose8(pa), w1 = transpose8(pb);
-          if (valid >= kKvTile) {
-#pragma unroll
-            for (int y = 0; y < NG; ++y) {
-              const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
-              const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
-              mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, w0, w1);
-              mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, w0, w1);
+            for (int o = 4; o < 32; o *= 2) {
+              n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, o));
+              n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, o));
             }
-          } else {
-            // V rows of tokens that are not there may hold anything: 0 * NaN is not 0
-            const uint32_t ka = (2 * t < valid ? 0xffffu : 0u) |
-                                (2 * t + 1 < valid ? 0xffff0000u : 0u);
-            const uint32_t kb = (2 * t + 8 < valid ? 0xffffu : 0u) |
-                                (2 * t + 9 < valid ? 0xffff0000u : 0u);
+            n0 = fmaxf(n0, m0);
+            n1 = fmaxf(n1, m1);
+            const float a0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+            const float a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            lim0 = (n0 + kSlack) * (1.f / qs0);
+            lim1 = (n1 + kSlack) * (1.f / qs1);
+            l0 *= a0;
+            l1 *= a1;
+            if constexpr (!kQuant) x0 *= a0, x1 *= a1;
+            float c0 = a0, c1 = a1;
+            if constexpr (kQuant) {
+              uint32_t top = 0;  // largest finite scale: bf16 bits order like the numbers
 #pragma unroll
-            for (int y = 0; y < NG; ++y) {
-              const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
-              const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
-              mma_bf16(acc[2 * y], va.x & ka, va.y & ka, vb.x & kb, vb.y & kb, w0, w1);
-              mma_bf16(acc[2 * y + 1], va.z & ka, va.w & ka, vb.z & kb, vb.w & kb, w0, w1);
+              for (int i = 0; i < TPS; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                  for (int w = 0; w < NG / 2; ++w) {
+                    const uint32_t lo = sv[i][r][w] & 0xffffu, hi = sv[i][r][w] >> 16;
+                    top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                  }
+              top = __reduce_max_sync(kFull, top);
+              const uint32_t ex = top >> 7;  // biased exponent
+              const float f = __uint_as_float(min(254u + kScaleSet - ex, 245u) << 23);
+              const int lim = static_cast<int>((ex + kScaleSlack + 1) << 7) - 1;
+              if (on0 && static_cast<int>(top) > vlim0) {
+                if (vlim0 >= 0) c0 *= f / vf0;
+                vf0 = f;
+                vlim0 = lim;
+              }
+              if (on1 && static_cast<int>(top) > vlim1) {
+                if (vlim1 >= 0) c1 *= f / vf1;
+                vf1 = f;
+                vlim1 = lim;
+              }
             }
+#pragma unroll
+            for (int n = 0; n < 2 * NG; ++n) {
+              acc[n][0] *= c0;
+              acc[n][1] *= c1;
+              acc[n][2] *= c0;
+              acc[n][3] *= c1;
+            }
+            asum[0] *= c0;
+            asum[1] *= c1;
+            asum[2] *= c0;
+            asum[3] *= c1;
           }
-        } else {
-          uint32_t vw[TPS][2][NG * L::WPG];
+          const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+          float p[TPS][4];
 #pragma unroll
           for (int i = 0; i < TPS; ++i) {
-            l0 += p[i][0] + p[i][2];
-            l1 += p[i][1] + p[i][3];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) p[i][n] *= n & 1 ? vf1 : vf0;
-#pragma unroll
-            for (int q = 0; q < L::PIECES; ++q) {
-              const uint4 x = *reinterpret_cast<const uint4*>(step + i * L::TILE_BYTES + L::CODES +
-                                                              q * 512 + lane * 16);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                vw[i][(q * 4 + n) / (NG * L::WPG)][(q * 4 + n) % (NG * L::WPG)] = w[n];
-            }
+            p[i][0] = ex2(fmaf(z[i][0], qs0, -b0));
+            p[i][1] = ex2(fmaf(z[i][1], qs1, -b1));
+            p[i][2] = ex2(fmaf(z[i][2], qs0, -b0));
+            p[i][3] = ex2(fmaf(z[i][3], qs1, -b1));
           }
+          // ---- O^T += V^T P: rows are channels, P^T is P transposed in registers
+          if constexpr (!kQuant) {
+            const unsigned char* vt = step + L::CODES;
+            x0 += p[0][0] + p[0][2];
+            x1 += p[0][1] + p[0][3];
+            const uint32_t pa = pack_bf16(p[0][0], p[0][1]), pb = pack_bf16(p[0][2], p[0][3]);
+            l0 += low16(pa) + low16(pb);
+            l1 += high16(pa) + high16(pb);
+            const uint32_t w0 = transpose8(pa), w1 = transpose8(pb);
+            if (valid >= kKvTile) {
 #pragma unroll
-          for (int y = 0; y < NG; ++y) {
-            const uint32_t one = g == y ? 0x3c003c00u : 0u;
+              for (int y = 0; y < NG; ++y) {
+                const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
+                const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
+                mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, w0, w1);
+                mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, w0, w1);
+              }
+            } else {
+              // V rows of tokens that are not there may hold anything: 0 * NaN is not 0
+              const uint32_t ka = (2 * t < valid ? 0xffffu : 0u) |
+                                  (2 * t + 1 < valid ? 0xffff0000u : 0u);
+              const uint32_t kb = (2 * t + 8 < valid ? 0xffffu : 0u) |
+                                  (2 * t + 9 < valid ? 0xffff0000u : 0u);
+#pragma unroll
+              for (int y = 0; y < NG; ++y) {
+                const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
+                const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
+                mma_bf16(acc[2 * y], va.x & ka, va.y & ka, vb.x & kb, vb.y & kb, w0, w1);
+                mma_bf16(acc[2 * y + 1], va.z & ka, va.w & ka, vb.z & kb, vb.w & kb, w0, w1);
+              }
+            }
+          } else {
+            uint32_t vw[TPS][2][NG * L::WPG];
 #pragma unroll
             for (int i = 0; i < TPS; ++i) {
-              const float s0 = y & 1 ? high16(sv[i][0][y / 2]) : low16(sv[i][0][y / 2]);
-              const float s1 = y & 1 ? high16(sv[i][1][y / 2]) : low16(sv[i][1][y / 2]);
-              const uint32_t w0 = transpose8(pack_f16(p[i][0] * s0, p[i][1] * s0));
-              const uint32_t w1 = transpose8(pack_f16(p[i][2] * s1, p[i][3] * s1));
-              mma_f16(asum, one, 0u, one, 0u, w0, w1);
-              if constexpr (FMT == STEM_KV_Q4) {
-                const uint32_t va = vw[i][0][y], vb = vw[i][1][y];
-                mma_f16(acc[2 * y], va & 0x000f000fu, va & 0x00f000f0u, vb & 0x000f000fu,
-                        vb & 0x00f000f0u, w0, w1);
-                mma_f16(acc[2 * y + 1], va >> 8 & 0x000f000fu, va >> 8 & 0x00f000f0u,
-                        vb >> 8 & 0x000f000fu, vb >> 8 & 0x00f000f0u, w0, w1);
-              } else {
+              l0 += p[i][0] + p[i][2];
+              l1 += p[i][1] + p[i][3];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const uint32_t va = vw[i][0][2 * y + x], vb = vw[i][1][2 * y + x];
-                  mma_f16(acc[2 * y + x], va & 0x00ff00ffu, va >> 8 & 0x00ff00ffu,
-                          vb & 0x00ff00ffu, vb >> 8 & 0x00ff00ffu, w0, w1);
+              for (int n = 0; n < 4; ++n) p[i][n] *= n & 1 ? vf1 : vf0;
+#pragma unroll
+              for (int q = 0; q < L::PIECES; ++q) {
+                const uint4 x = *reinterpret_cast<const uint4*>(step + i * L::TILE_BYTES + L::CODES +
+                                                                q * 512 + lane * 16);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                  vw[i][(q * 4 + n) / (NG * L::WPG)][(q * 4 + n) % (NG * L::WPG)] = w[n];
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < NG; ++y) {
+              const uint32_t one = g == y ? 0x3c003c00u : 0u;
+#pragma unroll
+              for (int i = 0; i < TPS; ++i) {
+                const float s0 = y & 1 ? high16(sv[i][0][y / 2]) : low16(sv[i][0][y / 2]);
+                const float s1 = y & 1 ? high16(sv[i][1][y / 2]) : low16(sv[i][1][y / 2]);
+                const uint32_t w0 = transpose8(pack_f16(p[i][0] * s0, p[i][1] * s0));
+                const uint32_t w1 = transpose8(pack_f16(p[i][2] * s1, p[i][3] * s1));
+                mma_f16(asum, one, 0u, one, 0u, w0, w1);
+                if constexpr (FMT == STEM_KV_Q4) {
+                  const uint32_t va = vw[i][0][y], vb = vw[i][1][y];
+                  mma_f16(acc[2 * y], va & 0x000f000fu, va & 0x00f000f0u, vb & 0x000f000fu,
+                          vb & 0x00f000f0u, w0, w1);
+                  mma_f16(acc[2 * y + 1], va >> 8 & 0x000f000fu, va >> 8 & 0x00f000f0u,
+                          vb >> 8 & 0x000f000fu, vb >> 8 & 0x00f000f0u, w0, w1);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const uint32_t va = vw[i][0][2 * y + x], vb = vw[i][1][2 * y + x];
+                    mma_f16(acc[2 * y + x], va & 0x00ff00ffu, va >> 8 & 0x00ff00ffu,
+                            vb & 0x00ff00ffu, vb >> 8 & 0x00ff00ffu, w0, w1);
+                  }
                 }
               }
             }
           }
         }
+        __syncwarp();
+        valid -= C::STEP;
+        stage = stage + 1 == C::STAGES ? 0 : stage + 1;
       }
+      cp_wait<0>();
       __syncwarp();
-      valid -= C::STEP;
-      stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-    }
-    cp_wait<0>();
-    __syncwarp();
     }
 
     // ---- numerators in units of V: o = sum_t p_t V_t relative to 2^m
@@ -1003,7 +1006,8 @@ struct Sizes {
   int64_t items, lists;
   size_t list, count, arrived, start, stat, part, total;
 };
-Sizes sizes_of(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq, int kcap, bool share) {
+Sizes sizes_of(int format, int D, int block, int Hkv, int max_blocks, int R, int Hq, int kcap,
+               bool share) {
   Sizes s;
   const int G = Hq / Hkv;
   s.tiles_h = (G + kHeadTile - 1) / kHeadTile;

@@ -21,6 +21,16 @@ __host__ __device__ __forceinline__ void decode_row(const KvCache& c, const Deco
   }
 }
 
+// Entries of a part where the number of all entries (below 2^31) sets it. As it is not less than an
+// at_once-th of them, items with n_i entries have sum ceil(n_i / chunk) <= items + at_once parts.
+// Half as much again as an even share: fewer items are cut, and the CTAs that come free take the rest.
+// (Ragged rows of 32 sequences: per-head lists of 16K at 16 bits, 101 us with 1.5 or 2 even shares, 111
+// with 1.25; a selection and its attention over 32K at 4 bits, 94 with 1.5, 96 with 2, 98 with 1.25.)
+__host__ __device__ __forceinline__ int part_entries(int total, int at_once, int least) {
+  const int chunk = static_cast<int>((total / 2 * int64_t{3} + at_once - 1) / at_once);
+  return chunk > least ? chunk : least;
+}
+
 __device__ __forceinline__ Entry entry_of(const KvCache& c, int seq, int j, uint32_t heads,
                                           int32_t* status) {
   const int page = kv_page(c, seq, j, status);

@@ -8,8 +8,8 @@
 A page holds one selection block of one sequence; the caller hands pages out by writing `table`
 [nseq, max_blocks]. Calls are asynchronous on `stream` (default: torch's current stream of the
 cache's device) and make that device current while they launch. Tensors that a call makes itself
-(outputs, workspace) are allocated on torch's current stream: a caller that passes another stream
-passes its own outputs and workspace too, or orders the two streams itself.
+(outputs, workspace) are made for that stream, as under torch.cuda.stream(stream); a caller that
+reads them on another stream orders the two.
 """
 
 from __future__ import annotations

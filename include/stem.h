@@ -433,8 +433,8 @@ size_t stem_cache_page_bytes(int D, int block, int format);
  * Writes the K and V rows of new tokens: row (s, h, t) of k and v (device, dtype bfloat16 or
  * float32; element ((s * strides[0]) + (h * strides[1]) + (t * strides[2]) + d, d contiguous) becomes
  * token pos[s] + t of sequence s, for t < count[s] (NULL: T for every sequence). pos and count are
- * device int32[nseq], 0 <= count[s] <= T. Strides are host values in elements, not negative, and
- * multiples of 16 bytes. Each block whose last token is written gets its summaries; tokens of it
+ * device int32[nseq], 0 <= count[s] <= T <= max_blocks * block. Strides are host values in elements,
+ * not negative, and multiples of 16 bytes. Each block whose last token is written gets its summaries; tokens of it
  * that came earlier are read back from the page. Writing a position again replaces it, so a caller
  * may take tokens back by appending at an earlier position. Two sequences of one call must not
  * write the same page. status as in stem_args_t.
@@ -453,7 +453,8 @@ int stem_cache_read(const stem_cache_t* c, void* k, void* v, int dtype, int T,
 /*
  * Arguments of a decode step: R query tokens ("rows"), each of one sequence of the cache. Several
  * rows may belong to one sequence (draft tokens), each with its own number of visible tokens.
- *   q [R, Hq, D], out [R, Hq, D]  bfloat16 (dtype STEM_F32 returns STEM_ERR_UNSUPPORTED)
+ *   q [R, Hq, D], out [R, Hq, D]  bfloat16 (dtype STEM_F32 returns STEM_ERR_UNSUPPORTED); at 8
+ *                                 and 4 bits, |q| < 2^115 (its scaling to fp16 ends there)
  *   lse [R, Hq] float32           optional: ln of the softmax denominator
  *   rows [R] int32                sequence of each row; NULL: row r is sequence r (R <= nseq)
  *   lens [R] int32                tokens that the row sees: 0 .. len - 1, its own K and V (appended

@@ -81,6 +81,21 @@ int main() {
           if (status != (ok ? 0 : STEM_ERR_ARG)) return fail("row status", seq, len);
         }
   }
+  // parts of the attention's items: as many as CTAs, however many entries (the totals a call may
+  // have end at 2^31 - 1)
+  for (int at_once : {296, 444, 592})
+    for (int total : {0, 1, 2, 295, 296, 297, 1 << 20, 1431655764, 1431655766, INT_MAX - 1,
+                      INT_MAX}) {
+      const int chunk = part_entries(total, at_once, 2);
+      if (chunk < 2) return fail("chunk", total, chunk);
+      for (long long n : {1ll, 2ll, 7ll, 4095ll, 4096ll}) {  // items of n entries, the last has the rest
+        const long long items = (total + n - 1) / n;
+        const long long last = total - (items - 1) * n;
+        const long long parts =
+            items == 0 ? 0 : (items - 1) * ((n + chunk - 1) / chunk) + (last + chunk - 1) / chunk;
+        if (parts > items + at_once) return fail("parts", total, parts);
+      }
+    }
   std::printf("ok\n");
   return 0;
 }

@@ -524,6 +524,78 @@ def test_attention_over_whole_long_sequences(fmt, rows_per_seq):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lens,share", [([200 * 64 - 5], "group"),  # many parts, joined by a kernel
+                                        ([600 * 64, 64 * 31 + 7, 1, 64 * 390], "group"),
+                                        ([64 * 150, 64 * 90 + 33], "head")])
+def test_attention_over_lists_of_many_parts(fmt, lens, share):
+    """A few long items: every block of ragged sequences, split over all the CTAs that there are."""
+    g = torch.Generator().manual_seed(len(lens))
+    D, block, G = 64, 64, 2
+    gpu, cpu = filled(fmt, D, block, 1, lens, g)
+    nb = [-(-n // block) for n in lens]
+    lists = [[list(range(n))] * G for n in nb]
+    if share == "head":
+        lists = [[x[0], x[0][::2]] for x in lists]
+    idx, cnt = as_tensors(lists, max(nb))
+    q = rows(g, len(lens), G, D)
+    out, lse = S.stem_decode_attn(gpu, q.to(DEV), i32(lens), idx, cnt, share=share)
+    check_attn(cpu, fmt, q, list(range(len(lens))), lens, lists, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_with_long_parts(fmt):
+    """So many rows that a CTA's part is longer than what it stages at a time, and rows between them
+    that keep nothing."""
+    g = torch.Generator().manual_seed(31)
+    D, block, nb, R = 64, 64, 300, 700
+    gpu, cpu = filled(fmt, D, block, 1, [nb * block - 9], g)
+    lens = [0 if r % 5 == 3 else (nb * block - 9 if r % 2 else 64 * 77) for r in range(R)]
+    every = [-(-n // block) for n in lens]
+    idx = torch.arange(nb, dtype=torch.int32, device=DEV).expand(R, 1, nb).contiguous()
+    cnt = i32(every)[:, None].contiguous()
+    q = rows(g, R, 1, D)
+    out, lse = S.stem_decode_attn(gpu, q.to(DEV), i32(lens), idx, cnt, share="group",
+                                  rows=i32([0] * R))
+    some = [0, 1, 3, 350, 351, R - 1]
+    check_attn(cpu, fmt, q[some], [0] * len(some), [lens[r] for r in some],
+               [[list(range(every[r]))] for r in some], out[some], lse[some])
+    none = [r for r in range(R) if lens[r] == 0]
+    assert not out[none].any() and (lse[none] == -math.inf).all()
+    same = [r for r in range(R) if lens[r] == 64 * 77 and r % 5 != 3]
+    at = slice(same[7], same[7] + 1)
+    one = S.stem_decode_attn(gpu, q[at].to(DEV), i32([64 * 77]), idx[:1], cnt[at], share="group")
+    assert torch.allclose(one[0].float(), out[at].float(), rtol=2 ** -6, atol=1e-3)
+
+
+@pytest.mark.parametrize("fmt", ["q8", "q4"])
+def test_every_quotient_of_two_bfloat16_significands(fmt):
+    """All 128 significands of the largest element against all of the others', at several ratios:
+    codes equal those of the division in 64 bits (ties to even)."""
+    D, block = 64, 64
+    top = torch.arange(128, 256, dtype=torch.float64).repeat_interleave(5)  # largest of the group
+    scale = (top.float() / ref.QMAX[fmt]).to(torch.bfloat16).double()
+    vals = torch.arange(128, 256, dtype=torch.float64)
+    blocks = []
+    for i in range(top.numel()):
+        r = 2.0 ** -(i % 5)
+        x = vals[torch.randperm(128, generator=torch.Generator().manual_seed(i))] * r
+        x = torch.minimum(x, top[i])
+        for part in x.reshape(-1, 31)[:4] if x.numel() % 31 == 0 else x[:124].reshape(4, 31):
+            blocks.append((torch.cat([top[i:i + 1], part]), scale[i]))
+    x = torch.stack([b[0] for b in blocks])
+    s = torch.stack([b[1] for b in blocks])
+    want = torch.round(x / s[:, None]).clamp(-ref.QMAX[fmt], ref.QMAX[fmt]) * s[:, None]
+    k = x.reshape(1, 1, -1, D).to(torch.bfloat16)
+    T = k.shape[2]
+    table, pages = make_table([-(-T // block)], -(-T // block))
+    gpu, _ = pair(pages, 1, D, block, fmt, table)
+    S.stem_cache_append(gpu, k.to(DEV), -k.to(DEV), i32([0]))
+    got, neg = S.stem_cache_read(gpu, i32([0]), T=T, dtype=torch.float32)
+    assert torch.equal(got.cpu().double().reshape(-1, 32), want)
+    assert torch.equal(neg, -got)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_a_head_is_untouched_by_blocks_it_does_not_keep(fmt):
     """Per-head lists: NaN and infinities in a block that one head keeps reach that head alone."""
     g = torch.Generator().manual_seed(4)
@@ -725,6 +797,45 @@ def test_captured_steps_replay_with_new_lengths_and_overlap():
                 assert torch.equal(x, y)
 
 
+def test_the_binding_refuses_wrong_tensors():
+    g = torch.Generator().manual_seed(14)
+    gpu, _ = filled("q8", 64, 64, 2, [300, 64], g)
+    m = S.make_method("exp", rho_min=0.3, tau=3.0, k_min=2)
+    budget, kcap = S.stem_decode_budget(gpu.max_blocks, m, DEV)
+    q, lens = rows(g, 2, 4, 64).to(DEV), i32([300, 64])
+
+    def no(error, match, fn, *args, **kw):
+        with pytest.raises(error, match=match):
+            fn(*args, **kw)
+
+    d = (gpu, q, lens, budget, kcap, m)
+    no(TypeError, "q must be", S.stem_decode, gpu, q.float(), *d[2:])
+    no(ValueError, "contiguous", S.stem_decode, gpu, q.transpose(0, 1).contiguous().transpose(0, 1),
+       *d[2:])
+    no(ValueError, "cuda", S.stem_decode, gpu, q.cpu(), *d[2:])
+    no(TypeError, "lens must be", S.stem_decode, gpu, q, lens.long(), budget, kcap, m)
+    no(ValueError, "shape", S.stem_decode, gpu, q, lens[:1], budget, kcap, m)
+    no(ValueError, "shape", S.stem_decode, gpu, q, lens, budget[:-1].contiguous(), kcap, m)
+    no(ValueError, "kcap", S.stem_decode, gpu, q, lens, budget, 0, m)
+    no(S.StemError, "invalid argument", S.stem_decode, gpu, q, lens, budget, 99, m)
+    no(ValueError, "both", S.stem_decode_select, *d, sel_idx=torch.empty(2, 4, kcap, device=DEV))
+    no(TypeError, "rows must be a tensor", S.stem_decode, *d, rows=[0, 1])
+    no(S.StemError, "workspace", S.stem_decode, *d,
+       workspace=torch.empty(512, dtype=torch.uint8, device=DEV))
+    no(TypeError, "PagedCache", S.stem_decode, None, *d[1:])
+    odd = S.make_method("exp", rho_min=0.3, tau=3.0, score="antidiag")
+    no(S.StemError, "limits", S.stem_decode, gpu, q, lens, budget, kcap, odd)
+    k = torch.zeros(2, 2, 5, 64, dtype=torch.bfloat16, device=DEV)
+    no(TypeError, "bfloat16 or float32", S.stem_cache_append, gpu, k.half(), k.half(), i32([0, 0]))
+    no(ValueError, "same shape", S.stem_cache_append, gpu, k, k[:, :, :4], i32([0, 0]))
+    turned = k.transpose(2, 3).contiguous().transpose(2, 3)
+    no(ValueError, "last dimension", S.stem_cache_append, gpu, turned, turned, i32([0, 0]))
+    wide = torch.zeros(2, 2, 5, 67, dtype=torch.bfloat16, device=DEV)[..., :64]
+    no(S.StemError, "invalid argument", S.stem_cache_append, gpu, wide, wide, i32([0, 0]))
+    no(ValueError, "k must be", S.stem_cache_append, gpu, k[:1], k[:1], i32([0, 0]))
+    no(ValueError, "T is needed", S.stem_cache_read, gpu, i32([0, 0]))
+
+
 def test_another_stream_and_given_buffers():
     g = torch.Generator().manual_seed(13)
     gpu, _ = filled("q8", 64, 64, 2, [300, 64], g)
@@ -741,3 +852,11 @@ def test_another_stream_and_given_buffers():
     st.synchronize()
     for x, y in zip(bufs, want):
         assert torch.equal(x, y)
+    # what a call makes itself belongs to its stream: freed, it serves that stream again
+    made = S.stem_decode(gpu, q, lens, budget, kcap, m, stream=st)
+    st.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(made, want))
+    ptrs = {x.data_ptr() for x in made}
+    del made
+    mine = [torch.empty(x.shape, dtype=x.dtype, device=DEV) for x in want]
+    assert ptrs.isdisjoint(x.data_ptr() for x in mine)
