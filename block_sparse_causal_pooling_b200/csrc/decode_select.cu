@@ -161,7 +161,8 @@ __device__ void pick(const double* key, int last, int want, Team<T>& s) {
   s.sync();
   for (int w = 0; w < T / 32; ++w) lo = fmin(lo, s.lo[w]), hi = fmax(hi, s.hi[w]);
   // (a product that rounds keeps the order: a larger key never falls into a lower interval)
-  const double scale = hi > lo ? (s.kBuckets - 1) / (hi - lo) : 0.0;
+  // (finite, so that no product with it is NaN, which is no bucket)
+  const double scale = hi > lo ? fmin((s.kBuckets - 1) / (hi - lo), 1e300) : 0.0;
   auto bucket = [&](double x) -> int {
     if (x == -INFINITY) return 0;
     if (x == INFINITY) return s.kBuckets - 1;
