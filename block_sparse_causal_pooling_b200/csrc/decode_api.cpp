@@ -82,6 +82,10 @@ int cache_rows(bool write, const stem_cache_t* c, void* k, void* v, int dtype, i
   for (int n = 0; n < 3; ++n)
     if (strides[n] < 0 || strides[n] * elt % 16 != 0) return STEM_ERR_ARG;
   if (c->nseq == 0 || T == 0) return STEM_OK;
+  // (rows that are written need places of their own)
+  if (!write && ((c->nseq > 1 && strides[0] == 0) || (c->Hkv > 1 && strides[1] == 0) ||
+                 (T > 1 && strides[2] == 0)))
+    return STEM_ERR_ARG;
   if ((rc = check_buffers(c)) != STEM_OK) return rc;
   if (!k || !v || !pos || !aligned(k, 16) || !aligned(v, 16) || !aligned(pos, 4) ||
       !aligned(count, 4) || !aligned(status, 4))

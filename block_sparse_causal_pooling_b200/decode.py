@@ -121,12 +121,14 @@ def stem_cache_read(cache: PagedCache, pos, count=None, k=None, v=None, T: Optio
     are left as they were."""
     if (k is None) != (v is None):
         raise ValueError("give both of k and v, or neither")
+    handle = _handle(cache, stream)
     if k is None:
         if T is None:
             raise ValueError("T is needed when k and v are not given")
-        k = torch.zeros((cache.nseq, cache.Hkv, T, cache.D), dtype=dtype, device=cache.device)
-        v = torch.zeros_like(k)
-    _decode.read(cache, k, v, pos, count, status, _handle(cache, stream))
+        with torch.cuda.stream(stream):  # (None: the current one)
+            k = torch.zeros((cache.nseq, cache.Hkv, T, cache.D), dtype=dtype, device=cache.device)
+            v = torch.zeros_like(k)
+    _decode.read(cache, k, v, pos, count, status, handle)
     return k, v
 
 
@@ -166,6 +168,8 @@ def stem_decode_attn(cache: PagedCache, q, lens, sel_idx, sel_cnt, share: str = 
     [R, Hq]. share "group": the query heads of a kv head have one list, that of the first. Returns
     (out [R, Hq, D] bf16, lse [R, Hq] float32)."""
     _code(_SHARES, share, "share")
+    if not (isinstance(sel_idx, torch.Tensor) and isinstance(sel_cnt, torch.Tensor)):
+        raise TypeError("sel_idx and sel_cnt must be tensors")
     if sel_idx.dim() != 3:
         raise ValueError(f"sel_idx must be [R, Hq, kcap], got {tuple(sel_idx.shape)}")
     return _decode.decode(_ATTEND, cache, q, lens, rows, None, sel_idx.shape[2],

@@ -434,8 +434,8 @@ size_t stem_cache_page_bytes(int D, int block, int format);
  * float32; element ((s * strides[0]) + (h * strides[1]) + (t * strides[2]) + d, d contiguous) becomes
  * token pos[s] + t of sequence s, for t < count[s] (NULL: T for every sequence). pos and count are
  * device int32[nseq], 0 <= count[s] <= T <= max_blocks * block. Strides are host values in elements,
- * not negative, and multiples of 16 bytes. Each block whose last token is written gets its summaries; tokens of it
- * that came earlier are read back from the page. Writing a position again replaces it, so a caller
+ * not negative, and multiples of 16 bytes. Each block whose last token is written gets its
+ * summaries; tokens of it that came earlier are read back from the page. Writing a position again replaces it, so a caller
  * may take tokens back by appending at an earlier position. Two sequences of one call must not
  * write the same page. status as in stem_args_t.
  */
@@ -444,8 +444,8 @@ int stem_cache_append(const stem_cache_t* c, const void* k, const void* v, int d
                       int32_t* status, void* stream);
 
 /* The values that tokens pos[s] .. pos[s] + count[s] - 1 stand for, into k and v (rounded to
- * bfloat16, or exact in float32). Arguments as
- * for stem_cache_append; rows t >= count[s] are left as they were. */
+ * bfloat16, or exact in float32). Arguments as for stem_cache_append, but no stride may be 0 along
+ * an axis of several rows; rows t >= count[s] are left as they were. */
 int stem_cache_read(const stem_cache_t* c, void* k, void* v, int dtype, int T,
                     const int64_t* strides, const int32_t* pos, const int32_t* count,
                     int32_t* status, void* stream);

@@ -121,6 +121,28 @@ def test_refusals_come_before_any_device_work():
             assert got == codes.get(case.split()[-1], S.STEM_ERR_ARG), (call, case)
 
 
+def test_rows_read_back_need_places_of_their_own():
+    """A stride of 0 would give several rows one place; with one row along it there is no other."""
+    code = PROBE.split("out = {}")[0] + """
+read, cases = L.stem_cache_read, {}
+for n in range(3):
+    st = [2048, 1024, 128]
+    st[n] = 0
+    cases[n] = rows(read, strides=st)
+    one = dict(c=cache(nseq=0) if n == 0 else cache(Hkv=1) if n == 1 else cache(), T=1 if n == 2 else 4)
+    cases[f"one {n}"] = rows(read, strides=st, **one)
+print(json.dumps(cases))
+"""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="", PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True,
+                       timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr
+    got = json.loads(r.stdout.strip().splitlines()[-1])
+    for n in range(3):
+        assert got[str(n)] == S.STEM_ERR_ARG, n
+        assert got[f"one {n}"] != S.STEM_ERR_ARG, n
+
+
 def test_sizes():
     for fmt in ("bf16", "q8", "q4"):
         for d in (64, 128):

@@ -834,6 +834,27 @@ def test_the_binding_refuses_wrong_tensors():
     no(S.StemError, "invalid argument", S.stem_cache_append, gpu, wide, wide, i32([0, 0]))
     no(ValueError, "k must be", S.stem_cache_append, gpu, k[:1], k[:1], i32([0, 0]))
     no(ValueError, "T is needed", S.stem_cache_read, gpu, i32([0, 0]))
+    one = k[:, :, :1].expand(2, 2, 5, 64)
+    no(S.StemError, "invalid argument", S.stem_cache_read, gpu, i32([0, 0]), k=one, v=one)
+    S.stem_cache_append(gpu, one, one, i32([64, 0]))  # (many readers are fine)
+    idx, cnt = S.stem_decode_select(gpu, q, lens, budget, kcap, m)
+    no(TypeError, "sel_cnt must be", S.stem_decode_attn, gpu, q, lens, idx, None)
+    no(TypeError, "sel_cnt must be", S.stem_decode_attn, gpu, q, lens, None, cnt)
+
+
+def test_rows_read_back_on_another_stream():
+    """The zeros behind a sequence's rows are written before the rows, on the call's stream: with the
+    current stream busy, nothing of it comes after them."""
+    g = torch.Generator().manual_seed(15)
+    gpu, _ = filled("q4", 64, 64, 2, [300, 64], g)
+    want = S.stem_cache_read(gpu, i32([3, 0]), i32([200, 64]), T=200)
+    pos, count = i32([3, 0]), i32([200, 64])
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)
+    got = S.stem_cache_read(gpu, pos, count, T=200, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_another_stream_and_given_buffers():
