@@ -29,9 +29,10 @@
 // sums are float32. Warps, then CTAs of one (row, kv head), are joined by (max, sum, numerator).
 //
 // Measured (B200; 16 sequences, 32 heads on 8 kv heads of 128, every block; device time in a graph),
-// at 4K, 8K, 16K and 32K tokens: 16 bits 56, 95, 173 and 329 us, 8 bits 42, 65, 111 and 205 us, 4 bits
-// 43, 57, 90 and 157 us; at 32K 6.5, 5.6 and 3.9 TB/s (a copy reaches 6.47). A line through the four
-// has a slope of 6.9, 6.1 and 4.6 TB/s and starts at 17, 18 and 25 us.
+// at 4K, 8K, 16K and 32K tokens: 16 bits 56, 95, 175 and 331 us, 8 bits 41, 63, 108 and 197 us, 4 bits
+// 33, 49, 81 and 144 us; at 32K 6.5, 5.8 and 4.2 TB/s (a copy reaches 6.47). A line through the four
+// has a slope of 6.8, 6.4 and 4.8 TB/s and starts at 17 to 18 us. Few rows are bound by latency, long
+// lists at 16 and 8 bits by HBM, at 4 bits by the instructions that unpack and scale.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -67,10 +68,14 @@ struct Cfg {
   using L = Kv<FMT, D>;
   static constexpr bool Q = FMT != STEM_KV_BF16;
   static constexpr int TPS = Q ? 2 : 1;  // tiles a warp takes at once
-  static constexpr int STAGES = FMT == STEM_KV_Q8 ? 2 : 3;
+  static constexpr int STAGES = 3;
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;
-  // CTAs an SM: as many as registers allow at 4 and 8 bits, and the rings at 16.
-  static constexpr int CTAS = FMT == STEM_KV_Q4 ? 4 : FMT == STEM_KV_Q8 ? 3 : 2;
+  // CTAs an SM: as many as the rings allow at 8 and 16 bits; at 4 bits, as many as have the registers
+  // that the kernel wants. More of them are no faster. (4 bits, 4 CTAs of 128 registers with some
+  // spilled: 94 us for 64 ragged rows of up to 32K where 3 take 90, 27.1 for 8 of up to 64K where 3
+  // take 24.1. 8 bits, 3 CTAs with rings of 2 steps: 43 us for 32 ragged rows of up to 16K, 57.4 for
+  // every block of 4 of up to 64K, where 2 with rings of 3 take 32 and 55.1.)
+  static constexpr int CTAS = FMT == STEM_KV_Q4 ? 3 : 2;
   static constexpr int STEP = kKvTile * TPS;  // tokens
   static constexpr int STEP_BYTES = TPS * L::TILE_BYTES;
   static constexpr int RING = STAGES * STEP_BYTES;  // a warp's

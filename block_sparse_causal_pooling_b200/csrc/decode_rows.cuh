@@ -24,8 +24,9 @@ __host__ __device__ __forceinline__ void decode_row(const KvCache& c, const Deco
 // Entries of a part where the number of all entries (below 2^31) sets it. As it is not less than an
 // at_once-th of them, items with n_i entries have sum ceil(n_i / chunk) <= items + at_once parts.
 // Half as much again as an even share: fewer items are cut, and the CTAs that come free take the rest.
-// (Ragged rows of 32 sequences: per-head lists of 16K at 16 bits, 101 us with 1.5 or 2 even shares, 111
-// with 1.25; a selection and its attention over 32K at 4 bits, 94 with 1.5, 96 with 2, 98 with 1.25.)
+// (With 1.25, 1.5 and 2 even shares: 32 ragged rows of per-head lists of up to 16K at 16 bits take 111,
+// 101 and 100 us; every block of 4 ragged rows of up to 64K at 8 bits 53, 55 and 64; a selection and
+// its attention of 64 rows of up to 32K at 4 bits 90 with each.)
 __host__ __device__ __forceinline__ int part_entries(int total, int at_once, int least) {
   const int chunk = static_cast<int>((total / 2 * int64_t{3} + at_once - 1) / at_once);
   return chunk > least ? chunk : least;
