@@ -297,6 +297,32 @@ def test_select_long_contexts(share, nb):
 
 
 @pytest.mark.parametrize("share", ["head", "group"])
+@pytest.mark.parametrize("nb,G,D", [(300, 4, 128), (30, 9, 64), (700, 2, 64)])
+def test_select_of_many_rows(share, nb, G, D):
+    """More rows than run at once (a kernel with fewer registers) choose as the definition does, and
+    as the same rows do in a small call."""
+    g = torch.Generator().manual_seed(nb)
+    block, Hkv, few = 64, 2, 12
+    table, pages = make_table([nb], nb, spare=0)
+    gpu, _ = pair(pages, Hkv, D, block, "q4", table)
+    kb, vn = fill_summaries(gpu, g)
+    q = rows(g, few, Hkv * G, D)
+    lens = [nb * block - 64 * (nb // few) * r - 5 * r for r in range(few)]
+    m = S.make_method("exp", rho_min=0.1, tau=8.0, k_min=3, share=share)
+    budget, kcap = S.stem_decode_budget(nb, m, DEV)
+    times = 400 // few
+    st = status_word()
+    idx, cnt = S.stem_decode_select(gpu, q.repeat(times, 1, 1).to(DEV), i32(lens * times), budget,
+                                    kcap, m, rows=i32([0] * (few * times)), status=st)
+    assert int(st) == 0
+    check_select(gpu, q, [0] * few, lens, budget.tolist(), kb, vn, table, share, "product", 0.0, True,
+                 idx[:few], cnt[:few], kcap)
+    one = S.stem_decode_select(gpu, q.to(DEV), i32(lens), budget, kcap, m, rows=i32([0] * few))
+    assert torch.equal(idx, one[0].repeat(times, 1, 1))
+    assert torch.equal(cnt, one[1].repeat(times, 1))
+
+
+@pytest.mark.parametrize("share", ["head", "group"])
 def test_select_ties_and_odd_summaries(share):
     """Blocks that share a page tie exactly: the lower index wins. Zero V norms (ln 0), NaN and
     infinite summaries rank as the definition says."""
