@@ -330,6 +330,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) select_kernel(const Args a) {
   uint32_t* mask = reinterpret_cast<uint32_t*>(acc + a.slice +
                                                lists_of(a.m.group, csize) * a.c.max_blocks);
 
+  // Another CTA's shared memory may be written only once that CTA runs, which its arrival here tells.
+  // The wait for it is behind the first scores, so that it hides behind the loads of a CTA that has
+  // blocks (one without any comes there at once). The barrier's phases that follow start after it.
+  cluster.barrier_arrive();
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
   if (rank == 0 && a.lists.list)
@@ -417,6 +421,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) select_kernel(const Args a) {
           score[(2 * t + 1) * a.slice + j - j0] = there[y] ? v[2 * y + 1] : -INFINITY;
         }
       }
+    }
+    if (h0 == 0) cluster.barrier_wait();  // (every CTA of the cluster runs)
+    if (scored) {
       __syncthreads();
       if (product_group) {
         // ---- each head's softmax denominator: a warp per head, then over the cluster
