@@ -447,8 +447,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) select_kernel(const Args a) {
           for (int c = 0; c < csize; ++c) top = fmax(top, s.top[c][tid]);
           if (!(top > -INFINITY)) top = 0.0;
           for (int c = 0; c < csize; ++c) {
-            const double base = s.top[c][tid] > -INFINITY ? s.top[c][tid] : 0.0;
-            sum += s.sum[c][tid] * exp(base - top);
+            // a CTA without a finite score (of a short row, say) has no part in it: its sum is 0 (or
+            // NaN), and exp(-top) may be infinite
+            const double there = s.top[c][tid];
+            sum += there > -INFINITY ? s.sum[c][tid] * exp(there - top) : s.sum[c][tid];
           }
           s.lse[tid] = top + log(sum);
         }

@@ -46,3 +46,24 @@ def test_select_of_short_rows_in_a_wide_table(share, metric, wide, Hkv):
     again = [S.stem_decode_select(gpu, dq, dl, budget, kcap, m) for _ in range(50)]
     for i, c in again:
         assert torch.equal(i, idx) and torch.equal(c, cnt)
+
+
+@pytest.mark.parametrize("wide", [100, 200, 700, 4096])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_select_of_scores_far_from_zero(wide, sign):
+    """Every score of every head near -960, or near 960, where exp of it is 0 or infinite in 64 bits too:
+    what decides are the differences, whatever share of the cluster's CTAs has a block of the row."""
+    g = torch.Generator().manual_seed(17)
+    D, block, G, n = 64, 64, 4, 100
+    table, pages = common.make_table([n], wide)
+    gpu, _ = common.pair(pages, 1, D, block, "q4", table)
+    kb, vn = common.fill_summaries(gpu, g, scale=0.2)
+    kb = kb + sign * 10.0
+    gpu.kbar.copy_(kb)
+    q = (12.0 + 0.1 * torch.randn(2, G, D, generator=g)).to(torch.bfloat16)
+    lens = [n * block - 3, 77 * block]
+    m = S.make_method("exp", rho_min=0.2, tau=4.0, k_min=3, share="group")
+    budget, kcap = S.stem_decode_budget(wide, m, DEV)
+    idx, cnt = S.stem_decode_select(gpu, q.to(DEV), i32(lens), budget, kcap, m, rows=i32([0, 0]))
+    common.check_select(gpu, q, [0, 0], lens, budget.tolist(), kb, vn, table, "group", "product", 0.0,
+                        True, idx, cnt, kcap)
