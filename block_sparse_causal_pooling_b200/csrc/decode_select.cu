@@ -305,9 +305,26 @@ struct Args {
 };
 
 // Lists that a CTA of a cluster picks in a pass, with keys of their own.
-__host__ __device__ __forceinline__ int lists_of(bool group, int csize) {
+__host__ __device__ constexpr int lists_of(bool group, int csize) {
   return csize == 1 ? 0 : group ? 1 : (kHeads + csize - 1) / csize;
 }
+
+// Dynamic shared memory of a launch (in the order that the kernel lays it out), and the most that any
+// launch takes: a cluster is no smaller than its slices of kMaxSlice blocks make it.
+constexpr size_t smem_bytes(int max_blocks, int csize, bool group) {
+  const size_t slice = (max_blocks + csize - 1) / csize;
+  return sizeof(double) * ((kHeads + 2) * slice +
+                           static_cast<size_t>(lists_of(group, csize)) * max_blocks) +
+         (static_cast<size_t>(max_blocks) + 7) / 4 * 4;
+}
+constexpr size_t kMaxSmem = smem_bytes(STEM_MAX_NB, kMaxCluster, false);
+constexpr bool below_most(int csize) {
+  return csize > kMaxCluster ||
+         (smem_bytes(std::min(csize * kMaxSlice, STEM_MAX_NB), csize, false) <= kMaxSmem &&
+          smem_bytes(std::min(csize * kMaxSlice, STEM_MAX_NB), csize, true) <= kMaxSmem &&
+          below_most(2 * csize));
+}
+static_assert(below_most(1), "kMaxSmem is the most");
 
 // CTAS: CTAs of an SM that the registers are shared out for, 2 or 4 (see launch_decode_select).
 template <int D, int CTAS>
@@ -556,10 +573,7 @@ cudaError_t launch_decode_select(const KvCache& c, int D, const DecodeRows& r,
           (lists_all * csize < sm_count() && c.max_blocks > csize * kSlice)))
     csize *= 2;
   const Args a{c, r, budget, metric, lists, (c.max_blocks + csize - 1) / csize};
-  const size_t bytes = sizeof(double) * (static_cast<size_t>(kHeads + 2) * a.slice +
-                                         static_cast<size_t>(lists_of(metric.group, csize)) *
-                                             c.max_blocks) +
-                       (static_cast<size_t>(c.max_blocks) + 7) / 4 * 4;
+  const size_t bytes = smem_bytes(c.max_blocks, csize, metric.group);
   // Where more CTAs are launched than run at once at 2 an SM, 4 of them with fewer registers each:
   // 64 rows of up to 16K with 32 heads on 8 take 15.8 us instead of 20.5 (lists of their own 13.7
   // instead of 17.5). Where all run at once the registers are worth more: 33.4 us instead of 36.5 for
@@ -567,8 +581,9 @@ cudaError_t launch_decode_select(const KvCache& c, int D, const DecodeRows& r,
   const bool many = lists_all * csize > 2 * sm_count();
   void (*kernel)(const Args) = D == 128 ? (many ? select_kernel<128, 4> : select_kernel<128, 2>)
                                         : (many ? select_kernel<64, 4> : select_kernel<64, 2>);
+  // (the same value in every call: another thread's, between this and the launch, changes nothing)
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(bytes));
+                                             static_cast<int>(kMaxSmem));
   if (e != cudaSuccess) return e;
   return launch_after(kernel, dim3(csize, c.Hkv, r.R), kThreads, bytes, csize, st, a);
 }

@@ -2,18 +2,23 @@
 the sequences in them, scores and values far from 1, several threads, against tests/decode_ref.py."""
 
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
 import torch
 
+from block_sparse_causal_pooling_b200 import build as libbuild
 from block_sparse_causal_pooling_b200 import decode as S
+from block_sparse_causal_pooling_b200 import stem as base
 from tests import decode_ref as ref
 from tests import test_gpu_decode as common
 
 pytestmark = pytest.mark.gpu
 
 DEV = common.DEV
+HERE = os.path.dirname(os.path.abspath(__file__))
 i32, rows, status_word = common.i32, common.rows, common.status_word
 
 
@@ -67,3 +72,16 @@ def test_select_of_scores_far_from_zero(wide, sign):
     idx, cnt = S.stem_decode_select(gpu, q.to(DEV), i32(lens), budget, kcap, m, rows=i32([0, 0]))
     common.check_select(gpu, q, [0, 0], lens, budget.tolist(), kb, vn, table, "group", "product", 0.0,
                         True, idx, cnt, kcap)
+
+
+def test_select_from_two_threads_over_tables_of_different_widths(tmp_path):
+    """A narrow table's launch asks for less shared memory than a wide one's, of the same kernel: what
+    one thread sets for its launch must not refuse another's."""
+    exe, lib = str(tmp_path / "threads"), os.path.dirname(base.LIB_PATH)
+    cmd = [libbuild._nvcc()] + libbuild.ARCH + ["-std=c++17", "-I", libbuild.INCLUDE, "-o", exe,
+                                                os.path.join(HERE, "decode_threads.cu"), "-L", lib,
+                                                "-l:libstem.so", "-Xlinker", "-rpath", "-Xlinker", lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout == "ok\n", r.stdout
