@@ -45,6 +45,14 @@ constexpr int kSelThreads = 256;
 constexpr int kWarps = kSelThreads / 32;
 constexpr int kTileJ = 64;
 
+// Lets a kernel (without static shared memory) have as much of it as an SM gives a CTA. The limit is the
+// kernel's, for all host threads: one that followed each call's need could be lowered by another
+// thread between that and the launch.
+template <typename... P>
+cudaError_t allow_smem(void (*kernel)(P...)) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+}
+
 __device__ __forceinline__ uint64_t order_bits(double x) {
   // order-preserving map from double to uint64 (no NaNs expected)
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));  // -0 -> +0
@@ -663,8 +671,7 @@ cudaError_t launch_group(const float* qbar, const float* kbar, const float* vnor
                                        kTileJ * (D + 4)) +
                       sizeof(int) * kWarps * 256;
   auto kern = select_group_kernel<D>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(B) * Hkv * ((nb + kGR - 1) / kGR);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -682,8 +689,7 @@ cudaError_t launch_rt(const float* qbar, const float* kbar, const float* vnorm, 
   const size_t smem = sizeof(float) * (static_cast<size_t>(R) * ldS + R * D + kTileJ * (D + 4)) +
                       sizeof(double) * ldS + sizeof(int) * kWarps * 256;
   auto kern = select_kernel<D, R>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   const int BH = B * Hq;
   const int64_t grid = static_cast<int64_t>(BH) * ((nb + R - 1) / R);
@@ -809,8 +815,7 @@ cudaError_t launch_p(const float* p, const float* vnorm, int B, int Hq, int Hkv,
   const size_t smem = sizeof(double) * (static_cast<size_t>(ldS) * (kGroup ? 1 + kWarps : 1)) +
                       sizeof(int) * kWarps * 256;
   auto kern = select_p_kernel<kGroup>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   const int64_t NH = kGroup ? static_cast<int64_t>(B) * Hkv : static_cast<int64_t>(B) * Hq;
   const int64_t grid = NH * ((nb + kWarps - 1) / kWarps);
@@ -848,8 +853,7 @@ cudaError_t launch_split(const float* qbar, const float* kbar, const float* vnor
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem1));
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(select_s_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem2));
+  e = allow_smem(select_s_kernel);
   if (e != cudaSuccess) return e;
   const int heads = B * Hq;
   for (int h0 = 0; h0 < heads; h0 += chunk) {
