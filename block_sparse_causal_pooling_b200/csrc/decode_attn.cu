@@ -14,9 +14,14 @@
 //      off_yh = -offset * sum_d q_d, is one more MMA, of the scales. q is scaled by a power of two per
 //      head so that its largest entry is in [2^14, 2^15): bf16's 8 significant bits survive in fp16.
 //   V: the scale goes to the weight: a_th = p_th s_t f rounded once to fp16, with f a power of two
-//      that follows the largest scale seen (like the running maximum of the softmax), so that no
-//      range of scales overflows or underflows. sum_t a_th (c_td - off) = sum a c - off * sum a; the
-//      last sum comes from one more MMA against a constant, so both sums see the same rounded a.
+//      that follows the largest scale seen (like the running maximum of the softmax), so that none
+//      overflows. sum_t a_th (c_td - off) = sum a c - off * sum a; the last sum comes from one more MMA
+//      against a constant, so both sums see the same rounded a. A weight below fp16's normal range is
+//      off by up to 2^-25, which the sum of a group's weights shows: where it is so small that n
+//      tokens could be off by 2^-12 of it together (a group of channels, or the tokens that a head
+//      looks at, far below the largest scale), the CTA goes over its entries again, first for the
+//      largest p s of each head and group, then with an f for each. So whatever the scales are, the
+//      weights are off by no more than 2^-11 of each and 2^-12 of their sum.
 // The tensor pipe cuts the products of a chain at 2^-25 of the largest and takes a subnormal's
 // exponent for -14 (measured), so a product keeps its bits down to 2^-15 code steps times the largest
 // q (or weight) of the chain. bf16 entries of q above 2^-8 of the largest lose nothing; the value sums
@@ -38,6 +43,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "decode_launch.h"
 #include "decode_rows.cuh"
@@ -57,11 +63,13 @@ constexpr int kStaged = 128;  // list entries in shared memory at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A logit may exceed the running maximum by this much (in log2 units) before the accumulators are
-// rescaled: weights stay below 2^8, and most steps need neither the warp's maximum nor a rescale.
-constexpr float kSlack = 8.f;
-// The V scales' power of two puts the largest scale in [2^3, 2^4) when it is set, and is set again
-// when a scale exceeds 2^7 in its units: weights stay below 2^15, fp16's range.
-constexpr int kScaleSet = 3, kScaleSlack = 3;
+// rescaled: weights stay below 2^5, and most steps need neither the warp's maximum nor a rescale.
+constexpr float kSlack = 5.f;
+// The V scales' power of two puts the largest scale in [2^6, 2^7) when it is set, and is set again
+// when a scale exceeds 2^10 in its units: weights stay below 2^15, fp16's range.
+constexpr int kScaleSet = 6, kScaleSlack = 3;
+// A sum of weights that n tokens may be off by 2^-12 of, at 2^-25 each, is below n times this.
+constexpr float kLeastSum = 0x1p-13f;
 
 template <int FMT, int D>
 struct Cfg {
@@ -495,23 +503,33 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
   float x0, x1;          // at 16 bits: sum of the weights before rounding
   float vf0, vf1;        // power of two of the V scales that each head meets
   int vlim0, vlim1;      // largest scales (bf16 bits) that they are good for
+  uint32_t seen[NG / 2];        // largest V scale (bf16 bits) of each group, two groups a word
+  float f0[kQuant ? NG : 1];    // going over the entries again: the largest p s of each group, then
+  float f1[kQuant ? NG : 1];    // the power of two that it gets
   unsigned char* ring = smem + warp * C::RING;
   const int spb_log = a.c.block / C::STEP == 2 ? 1 : a.c.block / C::STEP == 4 ? 2 : 3;
   const int64_t page_bytes = static_cast<int64_t>(a.c.Hkv) * a.c.record;
   const unsigned char* head_pages = a.c.at(0, kv) + lane * 16;
 
-  // Goes over the steps of the entries that one of `heads` keeps.
-  auto stream = [&](uint32_t heads) {
+  // Goes over the steps of the entries that one of `heads` keeps. again (at 8 and 4 bits): with the
+  // statistics as the first time left them, for the largest p s of each group into f0 and f1, or with
+  // weights in units of f0 and f1 (exact).
+  auto stream = [&](uint32_t heads, auto again, bool exact) {
+    constexpr bool kAgain = decltype(again)::value;
 #pragma unroll
     for (int n = 0; n < 2 * NG; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) asum[e] = 0.f;
-    m0 = m1 = lim0 = lim1 = -INFINITY;
-    l0 = l1 = x0 = x1 = 0.f;
-    vf0 = vf1 = 1.f;
-    vlim0 = vlim1 = -1;
+    if constexpr (!kAgain) {
+      m0 = m1 = lim0 = lim1 = -INFINITY;
+      l0 = l1 = x0 = x1 = 0.f;
+      vf0 = vf1 = 1.f;
+      vlim0 = vlim1 = -1;
+#pragma unroll
+      for (int w = 0; w < NG / 2; ++w) seen[w] = 0;
+    }
     for (int e0 = 0; e0 < n_ent; e0 += kStaged) {
       __syncthreads();
       const int n_now = min(n_ent - e0, kStaged);
@@ -651,77 +669,82 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
               }
           }
           // ---- running maximum and scale: exact only when a logit or a scale leaves its slack
-          float n0 = fmaxf(z[0][0], z[0][2]), n1 = fmaxf(z[0][1], z[0][3]);
-          bool move = false;
-          if constexpr (kQuant) {
-            n0 = fmaxf(n0, fmaxf(z[1][0], z[1][2]));
-            n1 = fmaxf(n1, fmaxf(z[1][1], z[1][3]));
-            uint32_t top = __vmaxu2(__vmaxu2(sv[0][0][0], sv[0][1][0]),
-                                    __vmaxu2(sv[1][0][0], sv[1][1][0]));
-            if constexpr (NG == 4)
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(sv[0][0][1], sv[0][1][1]),
-                                           __vmaxu2(sv[1][0][1], sv[1][1][1])));
-            const int most = static_cast<int>(max(top & 0xffffu, top >> 16));
-            move = (on0 && most > vlim0) || (on1 && most > vlim1);
-          }
-          move |= n0 > lim0 || n1 > lim1;
-          if (__any_sync(kFull, move)) {
-            n0 *= qs0;
-            n1 *= qs1;
-#pragma unroll
-            for (int o = 4; o < 32; o *= 2) {
-              n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, o));
-              n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, o));
-            }
-            n0 = fmaxf(n0, m0);
-            n1 = fmaxf(n1, m1);
-            const float a0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
-            const float a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-            m0 = n0;
-            m1 = n1;
-            lim0 = (n0 + kSlack) * (1.f / qs0);
-            lim1 = (n1 + kSlack) * (1.f / qs1);
-            l0 *= a0;
-            l1 *= a1;
-            if constexpr (!kQuant) x0 *= a0, x1 *= a1;
-            float c0 = a0, c1 = a1;
+          if constexpr (!kAgain) {
+            float n0 = fmaxf(z[0][0], z[0][2]), n1 = fmaxf(z[0][1], z[0][3]);
+            bool move = false;
             if constexpr (kQuant) {
-              uint32_t top = 0;  // largest finite scale: bf16 bits order like the numbers
+              n0 = fmaxf(n0, fmaxf(z[1][0], z[1][2]));
+              n1 = fmaxf(n1, fmaxf(z[1][1], z[1][3]));
+              uint32_t top = 0;
 #pragma unroll
-              for (int i = 0; i < TPS; ++i)
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                  for (int w = 0; w < NG / 2; ++w) {
-                    const uint32_t lo = sv[i][r][w] & 0xffffu, hi = sv[i][r][w] >> 16;
-                    top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                  }
-              top = __reduce_max_sync(kFull, top);
-              const uint32_t ex = top >> 7;  // biased exponent
-              const float f = __uint_as_float(min(254u + kScaleSet - ex, 245u) << 23);
-              const int lim = static_cast<int>((ex + kScaleSlack + 1) << 7) - 1;
-              if (on0 && static_cast<int>(top) > vlim0) {
-                if (vlim0 >= 0) c0 *= f / vf0;
-                vf0 = f;
-                vlim0 = lim;
+              for (int w = 0; w < NG / 2; ++w) {
+                const uint32_t here = __vmaxu2(__vmaxu2(sv[0][0][w], sv[0][1][w]),
+                                               __vmaxu2(sv[1][0][w], sv[1][1][w]));
+                seen[w] = __vmaxu2(seen[w], here);
+                top = w == 0 ? here : __vmaxu2(top, here);
               }
-              if (on1 && static_cast<int>(top) > vlim1) {
-                if (vlim1 >= 0) c1 *= f / vf1;
-                vf1 = f;
-                vlim1 = lim;
-              }
+              const int most = static_cast<int>(max(top & 0xffffu, top >> 16));
+              move = (on0 && most > vlim0) || (on1 && most > vlim1);
             }
+            move |= n0 > lim0 || n1 > lim1;
+            if (__any_sync(kFull, move)) {
+              n0 *= qs0;
+              n1 *= qs1;
 #pragma unroll
-            for (int n = 0; n < 2 * NG; ++n) {
-              acc[n][0] *= c0;
-              acc[n][1] *= c1;
-              acc[n][2] *= c0;
-              acc[n][3] *= c1;
+              for (int o = 4; o < 32; o *= 2) {
+                n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, o));
+                n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, o));
+              }
+              n0 = fmaxf(n0, m0);
+              n1 = fmaxf(n1, m1);
+              const float a0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+              const float a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+              m0 = n0;
+              m1 = n1;
+              lim0 = (n0 + kSlack) * (1.f / qs0);
+              lim1 = (n1 + kSlack) * (1.f / qs1);
+              l0 *= a0;
+              l1 *= a1;
+              if constexpr (!kQuant) x0 *= a0, x1 *= a1;
+              float c0 = a0, c1 = a1;
+              if constexpr (kQuant) {
+                uint32_t top = 0;  // largest finite scale: bf16 bits order like the numbers
+#pragma unroll
+                for (int i = 0; i < TPS; ++i)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int w = 0; w < NG / 2; ++w) {
+                      const uint32_t lo = sv[i][r][w] & 0xffffu, hi = sv[i][r][w] >> 16;
+                      top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                    }
+                top = __reduce_max_sync(kFull, top);
+                const uint32_t ex = top >> 7;  // biased exponent
+                const float f = __uint_as_float(min(254u + kScaleSet - ex, 245u) << 23);
+                const int lim = static_cast<int>((ex + kScaleSlack + 1) << 7) - 1;
+                if (on0 && static_cast<int>(top) > vlim0) {
+                  if (vlim0 >= 0) c0 *= f / vf0;
+                  vf0 = f;
+                  vlim0 = lim;
+                }
+                if (on1 && static_cast<int>(top) > vlim1) {
+                  if (vlim1 >= 0) c1 *= f / vf1;
+                  vf1 = f;
+                  vlim1 = lim;
+                }
+              }
+#pragma unroll
+              for (int n = 0; n < 2 * NG; ++n) {
+                acc[n][0] *= c0;
+                acc[n][1] *= c1;
+                acc[n][2] *= c0;
+                acc[n][3] *= c1;
+              }
+              asum[0] *= c0;
+              asum[1] *= c1;
+              asum[2] *= c0;
+              asum[3] *= c1;
             }
-            asum[0] *= c0;
-            asum[1] *= c1;
-            asum[2] *= c0;
-            asum[3] *= c1;
           }
           const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
           float p[TPS][4];
@@ -767,10 +790,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
             uint32_t vw[TPS][2][NG * L::WPG];
 #pragma unroll
             for (int i = 0; i < TPS; ++i) {
-              l0 += p[i][0] + p[i][2];
-              l1 += p[i][1] + p[i][3];
+              if constexpr (!kAgain) {
+                l0 += p[i][0] + p[i][2];
+                l1 += p[i][1] + p[i][3];
 #pragma unroll
-              for (int n = 0; n < 4; ++n) p[i][n] *= n & 1 ? vf1 : vf0;
+                for (int n = 0; n < 4; ++n) p[i][n] *= n & 1 ? vf1 : vf0;
+              }
 #pragma unroll
               for (int q = 0; q < L::PIECES; ++q) {
                 const uint4 x = *reinterpret_cast<const uint4*>(step + i * L::TILE_BYTES + L::CODES +
@@ -788,8 +813,23 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
               for (int i = 0; i < TPS; ++i) {
                 const float s0 = y & 1 ? high16(sv[i][0][y / 2]) : low16(sv[i][0][y / 2]);
                 const float s1 = y & 1 ? high16(sv[i][1][y / 2]) : low16(sv[i][1][y / 2]);
-                const uint32_t w0 = transpose8(pack_f16(p[i][0] * s0, p[i][1] * s0));
-                const uint32_t w1 = transpose8(pack_f16(p[i][2] * s1, p[i][3] * s1));
+                float a[4] = {p[i][0] * s0, p[i][1] * s0, p[i][2] * s1, p[i][3] * s1};
+                if constexpr (kAgain) {
+                  if (!exact) {  // (fmaxf leaves out the 0 * NaN of a masked token)
+                    f0[y] = fmaxf(f0[y], fmaxf(a[0], a[2]));
+                    f1[y] = fmaxf(f1[y], fmaxf(a[1], a[3]));
+                    continue;
+                  }
+#pragma unroll
+                  for (int n = 0; n < 4; ++n) {
+                    // (p s has passed float32's range only where f is below 1)
+                    const float f = n & 1 ? f1[y] : f0[y];
+                    a[n] = f < 1.f ? p[i][n] * ((n < 2 ? s0 : s1) * f) : a[n] * f;
+                    if (z[i][n] == -INFINITY) a[n] = 0.f;  // masked: whatever its scale
+                  }
+                }
+                const uint32_t w0 = transpose8(pack_f16(a[0], a[1]));
+                const uint32_t w1 = transpose8(pack_f16(a[2], a[3]));
                 mma_f16(asum, one, 0u, one, 0u, w0, w1);
                 if constexpr (FMT == STEM_KV_Q4) {
                   const uint32_t va = vw[i][0][y], vb = vw[i][1][y];
@@ -819,9 +859,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
 
     // ---- numerators in units of V: o = sum_t p_t V_t relative to 2^m
     if constexpr (kQuant) {
-      const float inv0 = 1.f / vf0, inv1 = 1.f / vf1;
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
+        const float inv0 = 1.f / (kAgain ? f0[y] : vf0), inv1 = 1.f / (kAgain ? f1[y] : vf1);
         const float off0 = static_cast<float>(L::OFFSET) * __shfl_sync(kFull, asum[0], 4 * y + t);
         const float off1 = static_cast<float>(L::OFFSET) * __shfl_sync(kFull, asum[1], 4 * y + t);
         // the second 8 rows of a 4-bit tile come from upper nibbles
@@ -837,12 +877,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
       x0 = l0;
       x1 = l1;
     }
+    if constexpr (!kAgain) {
 #pragma unroll
-    for (int o = 4; o < 32; o *= 2) {
-      l0 += __shfl_xor_sync(kFull, l0, o);
-      l1 += __shfl_xor_sync(kFull, l1, o);
-      x0 += __shfl_xor_sync(kFull, x0, o);
-      x1 += __shfl_xor_sync(kFull, x1, o);
+      for (int o = 4; o < 32; o *= 2) {
+        l0 += __shfl_xor_sync(kFull, l0, o);
+        l1 += __shfl_xor_sync(kFull, l1, o);
+        x0 += __shfl_xor_sync(kFull, x0, o);
+        x1 += __shfl_xor_sync(kFull, x1, o);
+      }
     }
   };
 
@@ -910,25 +952,65 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
     }
   };
 
-  stream(0xffu);
-  // A head that does not keep a block still meets its V rows with weight 0, and 0 * NaN or 0 * inf
-  // (of a 16-bit value or of a scale) is not 0. That shows as a NaN: such a CTA goes over its entries
-  // once more for each head alone, so that a head meets only blocks it keeps.
-  bool odd = false;
-  if (!a.share && nh > 1) {
-    bool nan = false;
+  stream(0xffu, std::false_type{}, false);
+  if constexpr (kQuant) {
+    // Weights that may be off (lane (y, t) has the sums of group y for heads 2t and 2t + 1), and the NaN
+    // of a weight 0 with a scale that is NaN, of a block that another head keeps.
 #pragma unroll
-    for (int n = 0; n < 2 * NG; ++n)
+    for (int w = 0; w < NG / 2; ++w)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) nan |= isnan(acc[n][e]);
-    odd = __syncthreads_or(nan);
-  }
-  if (!odd) {
+      for (int o = 4; o < 32; o *= 2) seen[w] = __vmaxu2(seen[w], __shfl_xor_sync(kFull, seen[w], o));
+    bool unsure = false;
+    if (g < NG && 2 * t < nh) {
+      const uint32_t pair = NG == 4 && g >= 2 ? seen[NG / 2 - 1] : seen[0];
+      const bool any = (g & 1 ? pair >> 16 : pair & 0xffffu) != 0;  // (not all of the group's V are 0)
+      const float least = static_cast<float>(n_ent) * (a.c.block / C::WARPS) * kLeastSum;
+      unsure = any && ((l0 > 0.f && asum[0] < least) || (l1 > 0.f && asum[1] < least));
+      unsure |= !a.share && (isnan(asum[0]) || isnan(asum[1]));
+    }
+    if (__syncthreads_or(unsure)) {
+#pragma unroll
+      for (int y = 0; y < NG; ++y) f0[y] = f1[y] = 0.f;
+      stream(0xffu, std::true_type{}, false);
+#pragma unroll
+      for (int y = 0; y < NG; ++y) {
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) {
+          f0[y] = fmaxf(f0[y], __shfl_xor_sync(kFull, f0[y], o));
+          f1[y] = fmaxf(f1[y], __shfl_xor_sync(kFull, f1[y], o));
+        }
+        // the largest weight to [2^14, 2^15), or below where it is infinite (less than 2^(5 + 126)) or
+        // next to nothing
+        auto power = [](float w) {
+          const int up = 14 + 127 - static_cast<int>(__float_as_uint(w) >> 23);
+          return __uint_as_float(static_cast<uint32_t>(127 + (isinf(w) ? -117 : min(up, 126))) << 23);
+        };
+        f0[y] = power(f0[y]);
+        f1[y] = power(f1[y]);
+      }
+      stream(0xffu, std::true_type{}, true);
+    }
     finish(0xffu);
   } else {
-    for (int h = 0; h < nh; ++h) {
-      stream(1u << h);
-      finish(1u << h);
+    // A head that does not keep a block still meets its V rows with weight 0, and 0 * NaN or 0 * inf is
+    // not 0. That shows as a NaN: such a CTA goes over its entries once more for each head alone, so
+    // that a head meets only blocks it keeps.
+    bool odd = false;
+    if (!a.share && nh > 1) {
+      bool nan = false;
+#pragma unroll
+      for (int n = 0; n < 2 * NG; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) nan |= isnan(acc[n][e]);
+      odd = __syncthreads_or(nan);
+    }
+    if (!odd) {
+      finish(0xffu);
+    } else {
+      for (int h = 0; h < nh; ++h) {
+        stream(1u << h, std::false_type{}, false);
+        finish(1u << h);
+      }
     }
   }
   // ---- of an item in parts, the CTA that brings the last one joins them

@@ -505,7 +505,10 @@ int stem_decode_select(const stem_decode_args_t* a, void* stream);
  * Softmax attention of each row over the tokens below lens of its kept blocks (sel_idx, sel_cnt:
  * distinct blocks in [0, i], in any order; with STEM_SHARE_GROUP the list of a kv head's first
  * query head serves all of them). 4- and 8-bit pages are read as they are: products of fp16
- * weights and exact codes, float32 sums. budget is not used.
+ * weights and exact codes, float32 sums. Each weight is off by up to 2^-11 of itself, and those of
+ * a group of 32 channels together by up to 2^-12 of their sum over the tokens, whatever the scales
+ * of other groups, other tokens or blocks that the head does not keep. The kept tokens times their
+ * largest |V| must stay below 2^122. budget is not used.
  */
 int stem_decode_attn(const stem_decode_args_t* a, void* stream);
 

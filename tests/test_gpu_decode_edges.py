@@ -85,3 +85,95 @@ def test_select_from_two_threads_over_tables_of_different_widths(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout == "ok\n", r.stdout
+
+
+# ------------------------------------------------------------------ attention
+
+
+def check_scaled(cpu, fmt, q, lists, n, out, lse):
+    """check_attn of one row whose V rows may be of any size. Its tolerance counts a weight's rounding to
+    fp16, 2^-11 of it; below fp16's normal range weights may together be off by 2^-12 of their sum in a
+    channel group, of values up to the largest of each token's group."""
+    D, G = q.shape[2], q.shape[1] // cpu.Hkv
+    for h in range(q.shape[1]):
+        k, v = cpu.tokens(0, h // G, lists[h], n)
+        o, z = ref.attend(q[0, h], k, v)
+        tol, dl = ref.attn_tolerance(q[0, h], k, v, fmt, o)
+        w = torch.softmax(k @ q[0, h].double() / math.sqrt(D), 0)
+        top = v.abs().reshape(-1, D // 32, 32).amax(-1, keepdim=True).expand(-1, -1, 32).reshape(-1, D)
+        err = (out[0, h].cpu().double() - o).abs()
+        assert torch.all(err <= tol + 2.0 ** -12 * (w @ top)), (h, float((err / (w @ top)).max()))
+        assert abs(float(lse[0, h]) - z) <= dl
+
+
+def one_sequence(fmt, D, block, k, v):
+    n = k.shape[2]
+    table, pages = common.make_table([-(-n // block)], -(-n // block))
+    gpu, cpu = common.pair(pages, k.shape[1], D, block, fmt, table)
+    S.stem_cache_append(gpu, k.to(DEV), v.to(DEV), i32([0]))
+    cpu.pages[:] = gpu.pages.cpu().numpy()
+    return gpu, cpu
+
+
+@pytest.mark.parametrize("fmt", ["q8", "q4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("powers", [(0, -9, -14, -20), (0, -30, -30, -30), (-40, 0, -60, 12),
+                                    (-60, 40, 0, -19)])
+def test_channel_groups_of_unlike_size(fmt, D, powers):
+    """Values of each group of 32 channels at a scale of its own: none costs another its digits, however
+    the weights are spread over the tokens."""
+    g = torch.Generator().manual_seed(33)
+    n, block = 1000, 64
+    size = 2.0 ** torch.tensor(powers[:D // 32], dtype=torch.float64).repeat_interleave(32)
+    k = rows(g, 1, 1, n, D)
+    v = (torch.randn(1, 1, n, D, generator=g).double() * size).to(torch.bfloat16)
+    gpu, cpu = one_sequence(fmt, D, block, k, v)
+    for mag in (0.0, 0.5, 4.0):
+        q = (rows(g, 1, 3, D).float() * mag).to(torch.bfloat16)
+        lists = [list(range(16)), [0, 3, 15], [15]]
+        idx, cnt = common.as_tensors([lists], 16)
+        out, lse = S.stem_decode_attn(gpu, q.to(DEV), i32([n]), idx, cnt)
+        check_scaled(cpu, fmt, q, lists, n, out, lse)
+
+
+@pytest.mark.parametrize("fmt", ["q8", "q4"])
+@pytest.mark.parametrize("power", [10, 25, 40])
+def test_a_large_value_that_hardly_weighs(fmt, power):
+    """One token with values 2^power times the others' and next to no weight: the others' digits stay,
+    for the heads that keep its block and for those that do not."""
+    g = torch.Generator().manual_seed(34)
+    D, n, block = 64, 700, 64
+    k, v = torch.randn(2, 1, 1, n, D, generator=g)
+    q = torch.ones(1, 4, D) + 0.1 * torch.randn(1, 4, D, generator=g)
+    at = 333
+    k[0, 0, at] = -1.5 * power / 12  # a logit some `power` below the others, in ln
+    v[0, 0, at] *= 2.0 ** power
+    q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+    gpu, cpu = one_sequence(fmt, D, block, k, v)
+    every = list(range(11))
+    lists = [every, every, [b for b in every if b != at // block], [at // block, 10]]
+    idx, cnt = common.as_tensors([lists], 11)
+    out, lse = S.stem_decode_attn(gpu, q.to(DEV), i32([n]), idx, cnt)
+    check_scaled(cpu, fmt, q, lists, n, out, lse)
+
+
+@pytest.mark.parametrize("fmt", ["q8", "q4"])
+def test_values_next_to_the_types_limits(fmt):
+    """Values from the smallest normal numbers to ones whose sum over the tokens is just finite, in the
+    same row."""
+    g = torch.Generator().manual_seed(35)
+    D, n, block = 128, 128, 64
+    size = 2.0 ** torch.tensor((-120, 112, -100, 0), dtype=torch.float64).repeat_interleave(32)
+    k = rows(g, 1, 1, n, D)
+    v = (torch.randn(1, 1, n, D, generator=g).double() * size).to(torch.bfloat16)
+    gpu, cpu = one_sequence(fmt, D, block, k, v)
+    q = rows(g, 1, 2, D)
+    lists = [[0, 1], [1]]
+    idx, cnt = common.as_tensors([lists], 2)
+    out, lse = S.stem_decode_attn(gpu, q.to(DEV), i32([n]), idx, cnt)
+    o = out[0].cpu().double()
+    for h in range(2):
+        kk, vv = cpu.tokens(0, 0, lists[h], n)
+        want, _ = ref.attend(q[0, h], kk, vv)
+        scaled = ref.attn_tolerance(q[0, h], kk, vv / size, fmt, want / size)[0]
+        assert torch.all((o[h] - want).abs() / size <= scaled + 2.0 ** -12 * 8)
