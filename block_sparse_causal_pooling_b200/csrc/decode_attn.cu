@@ -336,14 +336,15 @@ __device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, in
         float4 p[kAtOnce];
         const float4* src = reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(h) * D) + c;
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {  // (past the end: the last part again, with weight 0)
+        for (int i = 0; i < kAtOnce; ++i) {  // (past the end: the last part again, left out below)
           const int e = min(i0 + i * kHalves, n - 1);
           p[i] = __ldcg(src + static_cast<int64_t>(slot0 + s0 + e) * (kHeadTile * D / 4));
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
           const int e = i0 + i * kHalves;
-          const float f = e < n ? ex2(st[min(e, n - 1) * nh + h].x - base) : 0.f;
+          if (e >= n) continue;  // (not a weight of 0: the part may be infinite)
+          const float f = ex2(st[e * nh + h].x - base);
           x.x = fmaf(f, p[i].x, x.x);
           x.y = fmaf(f, p[i].y, x.y);
           x.z = fmaf(f, p[i].z, x.z);

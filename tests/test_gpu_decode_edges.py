@@ -177,3 +177,25 @@ def test_values_next_to_the_types_limits(fmt):
         want, _ = ref.attend(q[0, h], kk, vv)
         scaled = ref.attn_tolerance(q[0, h], kk, vv / size, fmt, want / size)[0]
         assert torch.all((o[h] - want).abs() / size <= scaled + 2.0 ** -12 * 8)
+
+
+def test_an_infinite_value_is_infinite_in_the_output():
+    """... of its channel, with the sign of the definition, at 16 bits (the others hold no infinity)."""
+    g = torch.Generator().manual_seed(37)
+    D, n = 64, 200
+    k, v = rows(g, 1, 1, n, D), rows(g, 1, 1, n, D)
+    v[0, 0, 70, 3], v[0, 0, 130, 9], v[0, 0, 5, 9] = float("inf"), float("-inf"), float("-inf")
+    v[0, 0, 6, 20], v[0, 0, 150, 20] = float("inf"), float("-inf")
+    gpu, cpu = one_sequence("bf16", D, 64, k, v)
+    q = rows(g, 1, 2, D)
+    lists = [[0, 1, 2, 3]] * 2
+    idx, cnt = common.as_tensors([lists], 4)
+    for share in ("head", "group"):
+        out, _ = S.stem_decode_attn(gpu, q.to(DEV), i32([n]), idx, cnt, share=share)
+        for h in range(2):
+            want, _ = ref.attend(q[0, h], *cpu.tokens(0, 0, lists[h], n))
+            got = out[0, h].cpu().double()
+            odd = ~torch.isfinite(want)
+            assert odd.sum() == 3 and torch.isfinite(got[~odd]).all()
+            assert torch.equal(got[odd].nan_to_num(0.0), want[odd].nan_to_num(0.0))
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
