@@ -26,8 +26,9 @@
 // exponent for -14 (measured), so a product keeps its bits down to 2^-15 code steps times the largest
 // q (or weight) of the chain. bf16 entries of q above 2^-8 of the largest lose nothing; the value sums
 // lose less than 2^-10 of the half step by which the code itself may be off.
-// At 16 bits the operands are bf16 as stored, P is rounded to bf16 and the normaliser sums the
-// rounded values.
+// At 16 bits the operands are bf16 as stored and each weight is two bf16 numbers (2^-15 of it are lost):
+// HBM bounds that kernel, so that its MMAs for V twice over cost little (32 ragged rows of per-head
+// lists of up to 16K 102.6 us, 101.2 with one number, which lost 2^-8 of each weight).
 //
 // A warp streams whole tiles (16 tokens of K and V, contiguous in the page) through a ring of its own
 // in shared memory with cp.async: no barrier between warps until the end. Softmax statistics and
@@ -155,6 +156,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float low16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// lo and hi as bf16 pairs that add up to them but for 2^-15 of each: their upper halves, and what is left
+// with 2^-20 more. So no second part of a weight is 0 or below 0 beside a first that is not: the two
+// times an infinite V value are infinite, not NaN.
+__device__ __forceinline__ void two_parts(float lo, float hi, uint32_t& first, uint32_t& second) {
+  first = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+  second = pack_bf16(fmaf(lo, 0x1p-20f, lo - low16(first)), fmaf(hi, 0x1p-20f, hi - high16(first)));
+}
+
 struct Args {
   KvCache c;
   DecodeRows r;
@@ -167,9 +176,9 @@ struct Args {
   int per_item, chunk, at_once;
   __nv_bfloat16* out;
   float* lse;
-  // Parts of items, a slot for each CTA: [slot][8] statistics (max in log2 units, sum for the output,
-  // sum for lse) and [slot][8][D] numerators.
-  float4* stat;
+  // Parts of items, a slot for each CTA: [slot][8] statistics (max in log2 units, sum) and [slot][8][D]
+  // numerators.
+  float2* stat;
   float* part;
   bool direct;     // the CTA that brings an item's last part joins them
   int32_t* start;  // [items]: the item's first CTA; [items]: the chunk (where neither is fixed)
@@ -299,13 +308,13 @@ constexpr int kJoinStaged = 512;
 // straight-line code for the first time costs more than running it.)
 template <int D, int WARPS>
 __device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, int parts,
-                                        float4* st, int slot0) {
+                                        float2* st, int slot0) {
   constexpr int kLanes = D / 4, kHalves = 32 / kLanes, kAtOnce = 8;
   const int lane = threadIdx.x % 32, c = lane % kLanes, half = lane / kLanes;
   const int most = kJoinStaged / nh;  // parts staged at a time
   for (int h0 = 0; h0 < nh; h0 += WARPS) {
     const int h = min(h0 + static_cast<int>(threadIdx.x) / 32, nh - 1);  // (the last one twice)
-    float m = -INFINITY, l = 0.f, lx = 0.f;
+    float m = -INFINITY, l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int s0 = 0; s0 < parts; s0 += most) {
@@ -322,14 +331,12 @@ __device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, in
       for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
       const float base = top == -INFINITY ? 0.f : top, f0 = ex2(m - base);
       m = top;
-      l *= f0, lx *= f0;
+      l *= f0;
       x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
 #pragma unroll 1
       for (int s = lane; s < n; s += 32) {
-        const float4 v = st[s * nh + h];
-        const float f = ex2(v.x - base);
-        l = fmaf(f, v.y, l);
-        lx = fmaf(f, v.z, lx);
+        const float2 v = st[s * nh + h];
+        l = fmaf(ex2(v.x - base), v.y, l);
       }
 #pragma unroll 1
       for (int i0 = half; i0 < n; i0 += kAtOnce * kHalves) {
@@ -353,10 +360,7 @@ __device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, in
       }
     }
 #pragma unroll
-    for (int o = 16; o; o /= 2) {
-      l += __shfl_xor_sync(kFull, l, o);
-      lx += __shfl_xor_sync(kFull, lx, o);
-    }
+    for (int o = 16; o; o /= 2) l += __shfl_xor_sync(kFull, l, o);
     if (kHalves == 2) {
       x.x += __shfl_xor_sync(kFull, x.x, 16);
       x.y += __shfl_xor_sync(kFull, x.y, 16);
@@ -367,7 +371,7 @@ __device__ __noinline__ void join_parts(const Args& a, int64_t head0, int nh, in
     if (half == 0)
       *reinterpret_cast<uint2*>(a.out + (head0 + h) * D + 4 * c) =
           make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-    if (lane == 0 && a.lse) a.lse[head0 + h] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+    if (lane == 0 && a.lse) a.lse[head0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
   __shared__ int s_sum[C::WARPS];
   __shared__ bool s_last;
   __shared__ Entry ent[kStaged];
-  __shared__ float s_m[C::WARPS][kHeadTile], s_l[C::WARPS][kHeadTile], s_x[C::WARPS][kHeadTile];
+  __shared__ float s_m[C::WARPS][kHeadTile], s_l[C::WARPS][kHeadTile];
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int G = a.r.Hq / a.c.Hkv;
@@ -501,7 +505,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
   float asum[4];         // row y: sum of group y's weights
   float m0, m1, l0, l1;  // running maximum (log2 units) and sum of the weights as the MMA sees them
   float lim0, lim1;      // largest logits (as the MMA gives them) within the maximum's slack
-  float x0, x1;          // at 16 bits: sum of the weights before rounding
   float vf0, vf1;        // power of two of the V scales that each head meets
   int vlim0, vlim1;      // largest scales (bf16 bits) that they are good for
   uint32_t seen[NG / 2];        // largest V scale (bf16 bits) of each group, two groups a word
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
     for (int e = 0; e < 4; ++e) asum[e] = 0.f;
     if constexpr (!kAgain) {
       m0 = m1 = lim0 = lim1 = -INFINITY;
-      l0 = l1 = x0 = x1 = 0.f;
+      l0 = l1 = 0.f;
       vf0 = vf1 = 1.f;
       vlim0 = vlim1 = -1;
 #pragma unroll
@@ -706,7 +709,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
               lim1 = (n1 + kSlack) * (1.f / qs1);
               l0 *= a0;
               l1 *= a1;
-              if constexpr (!kQuant) x0 *= a0, x1 *= a1;
               float c0 = a0, c1 = a1;
               if constexpr (kQuant) {
                 uint32_t top = 0;  // largest finite scale: bf16 bits order like the numbers
@@ -759,33 +761,29 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
           // ---- O^T += V^T P: rows are channels, P^T is P transposed in registers
           if constexpr (!kQuant) {
             const unsigned char* vt = step + L::CODES;
-            x0 += p[0][0] + p[0][2];
-            x1 += p[0][1] + p[0][3];
-            const uint32_t pa = pack_bf16(p[0][0], p[0][1]), pb = pack_bf16(p[0][2], p[0][3]);
-            l0 += low16(pa) + low16(pb);
-            l1 += high16(pa) + high16(pb);
+            l0 += p[0][0] + p[0][2];
+            l1 += p[0][1] + p[0][3];
+            uint32_t pa, pb, ra, rb;
+            two_parts(p[0][0], p[0][1], pa, ra);
+            two_parts(p[0][2], p[0][3], pb, rb);
             const uint32_t w0 = transpose8(pa), w1 = transpose8(pb);
-            if (valid >= kKvTile) {
+            const uint32_t r0 = transpose8(ra), r1 = transpose8(rb);
+            // V rows of tokens that are not there may hold anything: 0 * NaN is not 0
+            uint32_t ka = kFull, kb = kFull;
+            if (valid < kKvTile) {
+              ka = (2 * t < valid ? 0xffffu : 0u) | (2 * t + 1 < valid ? 0xffff0000u : 0u);
+              kb = (2 * t + 8 < valid ? 0xffffu : 0u) | (2 * t + 9 < valid ? 0xffff0000u : 0u);
+            }
 #pragma unroll
-              for (int y = 0; y < NG; ++y) {
-                const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
-                const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
-                mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, w0, w1);
-                mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, w0, w1);
-              }
-            } else {
-              // V rows of tokens that are not there may hold anything: 0 * NaN is not 0
-              const uint32_t ka = (2 * t < valid ? 0xffffu : 0u) |
-                                  (2 * t + 1 < valid ? 0xffff0000u : 0u);
-              const uint32_t kb = (2 * t + 8 < valid ? 0xffffu : 0u) |
-                                  (2 * t + 9 < valid ? 0xffff0000u : 0u);
-#pragma unroll
-              for (int y = 0; y < NG; ++y) {
-                const uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
-                const uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
-                mma_bf16(acc[2 * y], va.x & ka, va.y & ka, vb.x & kb, vb.y & kb, w0, w1);
-                mma_bf16(acc[2 * y + 1], va.z & ka, va.w & ka, vb.z & kb, vb.w & kb, w0, w1);
-              }
+            for (int y = 0; y < NG; ++y) {
+              uint4 va = *reinterpret_cast<const uint4*>(vt + L::word(0, y, 0, lane));
+              uint4 vb = *reinterpret_cast<const uint4*>(vt + L::word(1, y, 0, lane));
+              va.x &= ka, va.y &= ka, va.z &= ka, va.w &= ka;
+              vb.x &= kb, vb.y &= kb, vb.z &= kb, vb.w &= kb;
+              mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, w0, w1);
+              mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, w0, w1);
+              mma_bf16(acc[2 * y], va.x, va.y, vb.x, vb.y, r0, r1);
+              mma_bf16(acc[2 * y + 1], va.z, va.w, vb.z, vb.w, r0, r1);
             }
           } else {
             uint32_t vw[TPS][2][NG * L::WPG];
@@ -875,16 +873,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
           acc[n][3] = (acc[n][3] * second - off1) * inv1;
         }
       }
-      x0 = l0;
-      x1 = l1;
     }
     if constexpr (!kAgain) {
 #pragma unroll
       for (int o = 4; o < 32; o *= 2) {
         l0 += __shfl_xor_sync(kFull, l0, o);
         l1 += __shfl_xor_sync(kFull, l1, o);
-        x0 += __shfl_xor_sync(kFull, x0, o);
-        x1 += __shfl_xor_sync(kFull, x1, o);
       }
     }
   };
@@ -895,7 +889,6 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
     if (g == 0) {
       s_m[warp][2 * t] = m0, s_m[warp][2 * t + 1] = m1;
       s_l[warp][2 * t] = l0, s_l[warp][2 * t + 1] = l1;
-      s_x[warp][2 * t] = x0, s_x[warp][2 * t + 1] = x1;
     }
     float* o = o_s + warp * kHeadTile * D;
 #pragma unroll
@@ -913,20 +906,19 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
 #pragma unroll
       for (int w = 1; w < C::WARPS; ++w) m = fmaxf(m, s_m[w][tid]);
       const float base = m == -INFINITY ? 0.f : m;
-      float l = 0.f, lx = 0.f;
+      float l = 0.f;
 #pragma unroll
       for (int w = 0; w < C::WARPS; ++w) {  // (a warp that saw nothing of the head weighs 0)
         const float f = ex2(s_m[w][tid] - base);
         s_m[w][tid] = f;
         l = fmaf(f, s_l[w][tid], l);
-        lx = fmaf(f, s_x[w][tid], lx);
       }
       if (heads >> tid & 1) {
         s_l[0][tid] = l == 0.f ? 0.f : 1.f / l;
         if (!whole)
-          a.stat[slot * kHeadTile + tid] = make_float4(m, l, lx, 0.f);
+          a.stat[slot * kHeadTile + tid] = make_float2(m, l);
         else if (a.lse && tid < nh)
-          a.lse[head0 + tid] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+          a.lse[head0 + tid] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
     }
     __syncthreads();
@@ -1022,7 +1014,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
     __syncthreads();
     if (s_last) {
       __threadfence();  // (the other CTAs' parts are visible)
-      join_parts<D, C::WARPS>(a, head0, nh, parts, reinterpret_cast<float4*>(smem), first);
+      join_parts<D, C::WARPS>(a, head0, nh, parts, reinterpret_cast<float2*>(smem), first);
     }
   }
 }
@@ -1035,7 +1027,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   constexpr int kGroups = kJoinThreads / D, kJoinWarps = kJoinThreads / 32;
   extern __shared__ float weight[];  // [most]
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_x[kJoinWarps], s_o[kGroups][D];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_o[kGroups][D];
   const int row = blockIdx.y, head = blockIdx.x, tid = threadIdx.x;
   const int G = a.r.Hq / a.c.Hkv, h = head % G % kHeadTile;
   const int item = (row * a.c.Hkv + head / G) * a.lists.tiles_h + head % G / kHeadTile;
@@ -1054,19 +1046,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
   const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, lx = 0.f;
+  float l = 0.f;
   for (int s = tid; s < parts; s += kJoinThreads) {
-    const float4 st = a.stat[(slot0 + s) * kHeadTile + h];
+    const float2 st = a.stat[(slot0 + s) * kHeadTile + h];
     const float f = ex2(st.x - base);
     weight[s] = f;
     l = fmaf(f, st.y, l);
-    lx = fmaf(f, st.z, lx);
   }
-  for (int o = 16; o; o /= 2) {
-    l += __shfl_xor_sync(kFull, l, o);
-    lx += __shfl_xor_sync(kFull, lx, o);
-  }
-  if (tid % 32 == 0) s_l[tid / 32] = l, s_x[tid / 32] = lx;
+  for (int o = 16; o; o /= 2) l += __shfl_xor_sync(kFull, l, o);
+  if (tid % 32 == 0) s_l[tid / 32] = l;
   __syncthreads();
   const int d = tid % D, grp = tid / D;
   const float* part = a.part + static_cast<int64_t>(h) * D + d;
@@ -1077,14 +1065,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Args a) {
   s_o[grp][d] = x;
   __syncthreads();
   if (grp == 0) {
-    l = s_l[0], lx = s_x[0];
+    l = s_l[0];
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) l += s_l[w], lx += s_x[w];
+    for (int w = 1; w < kJoinWarps; ++w) l += s_l[w];
 #pragma unroll
     for (int i = 1; i < kGroups; ++i) x += s_o[i][d];
     const int64_t o = static_cast<int64_t>(row) * a.r.Hq + head;
     a.out[o * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-    if (d == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+    if (d == 0 && a.lse) a.lse[o] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -1131,7 +1119,7 @@ Sizes sizes_of(int format, int D, int block, int Hkv, int max_blocks, int R, int
   const size_t slots = static_cast<size_t>(s.ctas);
   s.arrived = take(sizeof(int32_t) * static_cast<size_t>(s.items));
   s.start = take(sizeof(int32_t) * static_cast<size_t>(s.items + 1));
-  s.stat = take(sizeof(float4) * slots * kHeadTile);
+  s.stat = take(sizeof(float2) * slots * kHeadTile);
   s.part = take(sizeof(float) * slots * kHeadTile * D);
   s.total = o;
   return s;
@@ -1140,7 +1128,7 @@ Sizes sizes_of(int format, int D, int block, int Hkv, int max_blocks, int R, int
 template <int FMT, int D>
 cudaError_t launch(const Args& a, int ctas, bool planned, cudaStream_t st) {
   using C = Cfg<FMT, D>;
-  static_assert(C::RING >= kHeadTile * D * 4 && C::WARPS * C::RING >= kJoinStaged * 16,
+  static_assert(C::RING >= kHeadTile * D * 4 && C::WARPS * C::RING >= kJoinStaged * sizeof(float2),
                 "the rings hold the warps' results, then the parts' statistics, at the end");
   cudaError_t e = cudaSuccess;
   if (!planned) {
@@ -1191,7 +1179,7 @@ cudaError_t launch_decode_attn(const KvCache& c, int format, int D, const Decode
   a.lse = lse;
   a.direct = std::min(s.ctas, s.at_once) <= kDirect * s.items;
   a.start = reinterpret_cast<int32_t*>(ws + s.start);
-  a.stat = reinterpret_cast<float4*>(ws + s.stat);
+  a.stat = reinterpret_cast<float2*>(ws + s.stat);
   a.part = reinterpret_cast<float*>(ws + s.part);
   if (D == 128) {
     switch (format) {

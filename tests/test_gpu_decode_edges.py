@@ -199,3 +199,30 @@ def test_an_infinite_value_is_infinite_in_the_output():
             assert odd.sum() == 3 and torch.isfinite(got[~odd]).all()
             assert torch.equal(got[odd].nan_to_num(0.0), want[odd].nan_to_num(0.0))
             assert torch.equal(torch.isnan(got), torch.isnan(want))
+
+
+@pytest.mark.parametrize("D,block", common.SHAPES)
+def test_weights_at_16_bits_keep_the_digits_of_float32(D, block):
+    """At 16 bits nothing but the output is rounded to bf16: what its own rounding leaves is 2^-15 of the
+    weights, beside the float32 steps (of 2^-22, as in attn_tolerance)."""
+    g = torch.Generator().manual_seed(36)
+    n = 5 * block + 9
+    k, v = rows(g, 1, 1, n, D), rows(g, 1, 1, n, D)
+    gpu, cpu = one_sequence("bf16", D, block, k, v)
+    q = rows(g, 1, 8, D)
+    lists = [list(range(6)), [0, 5], [5], [1, 2, 3], [0], [0, 1, 2, 4, 5], [4], [3, 5]]
+    idx, cnt = common.as_tensors([lists], 6)
+    out, lse = S.stem_decode_attn(gpu, q.to(DEV), i32([n]), idx, cnt)
+    u = 2.0 ** -22
+    for h in range(8):
+        kk, vv = cpu.tokens(0, 0, lists[h], n)
+        o, z = ref.attend(q[0, h], kk, vv)
+        m = kk.shape[0]
+        logits = kk @ q[0, h].double() / math.sqrt(D)
+        dz = (D + 4) * u * float((kk.abs() @ q[0, h].double().abs()).max()) / math.sqrt(D)
+        dz += 4 * u * float(logits.abs().max()) + 8 * u
+        w = torch.softmax(logits, 0)
+        tol = (w @ vv.abs()) * (2 * dz + 2.0 ** -15 + 2.0 ** -20 + (m // 16 + m + 40) * 2 * u)
+        err = (out[0, h].cpu().double() - o).abs()
+        assert torch.all(err <= tol + 2.0 ** -8 * (o.abs() + tol)), (h, float((err / o.abs()).max()))
+        assert abs(float(lse[0, h]) - z) <= dz + (m // 16 + m % 16 + 40) * u
