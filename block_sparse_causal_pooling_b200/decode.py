@@ -20,9 +20,9 @@ from typing import Optional
 import torch
 
 from . import stem as _stem
-from .stem import (STEM_KV_BF16, STEM_KV_Q4, STEM_KV_Q8, STEM_SHARE_GROUP, STEM_SHARE_HEAD,
-                   STEM_VSUM_MAX, STEM_VSUM_MEAN, StemError, make_method, stem_budget_m,
-                   stem_method_t)
+from .stem import (STEM_KV_BF16, STEM_KV_Q4, STEM_KV_Q8, STEM_SCHED_LINEAR, STEM_SHARE_GROUP,
+                   STEM_SHARE_HEAD, STEM_VSUM_MAX, STEM_VSUM_MEAN, StemError, make_method,
+                   stem_budget_m, stem_method_t)
 
 try:  # (after stem: libstem.so is loaded)
     from . import _decode
@@ -137,8 +137,12 @@ def stem_cache_read(cache: PagedCache, pos, count=None, k=None, v=None, T: Optio
 
 def stem_decode_budget(max_blocks: int, method: stem_method_t, device):
     """(budget [max_blocks] int32 on `device`, kcap): k(i) of the method's schedule for a query in
-    block i, and its largest value. Made once per method and context size."""
+    block i, and its largest value. Made once per method and table. The linear schedule runs over a
+    context's blocks, and a token is in the last block of its own: k(i) is that of the last block of
+    i + 1, however wide the table is."""
     k, _ = stem_budget_m(max_blocks, method)
+    if method.schedule == STEM_SCHED_LINEAR:
+        k = torch.minimum(k[-1], torch.arange(1, max_blocks + 1, dtype=torch.int32))
     return k.to(device), max(int(k.max()), 1)
 
 

@@ -459,7 +459,8 @@ int stem_cache_read(const stem_cache_t* c, void* k, void* v, int dtype, int T,
  *   rows [R] int32                sequence of each row; NULL: row r is sequence r (R <= nseq)
  *   lens [R] int32                tokens that the row sees: 0 .. len - 1, its own K and V (appended
  *                                 before) among them. 0: nothing is kept, out is 0, lse -infinity
- *   budget [max_blocks] int32     k(i), as from stem_budget_m, on the device
+ *   budget [max_blocks] int32     k(i), as from stem_budget_m, on the device (linear schedule: as the
+ *                                 last of a call with nb = i + 1, the context that ends in block i)
  *   kcap                          entries of a list, at least the largest k(i) in use; <= max_blocks
  *   sel_idx [R, Hq, kcap], sel_cnt [R, Hq] int32   kept blocks of each row and head, ascending;
  *                                 entries past sel_cnt are -1

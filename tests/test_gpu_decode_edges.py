@@ -226,3 +226,21 @@ def test_weights_at_16_bits_keep_the_digits_of_float32(D, block):
         err = (out[0, h].cpu().double() - o).abs()
         assert torch.all(err <= tol + 2.0 ** -8 * (o.abs() + tol)), (h, float((err / o.abs()).max()))
         assert abs(float(lse[0, h]) - z) <= dz + (m // 16 + m % 16 + 40) * u
+
+
+@pytest.mark.parametrize("wide", [60, 900])
+def test_select_with_the_linear_schedule(wide):
+    """Rows of a context keep as many blocks in a wide table as in one that fits."""
+    g = torch.Generator().manual_seed(41)
+    table, pages = common.make_table([60], wide)
+    gpu, _ = common.pair(pages, 1, 64, 64, "q8", table)
+    kb, vn = common.fill_summaries(gpu, g)
+    q = rows(g, 4, 4, 64)
+    lens = [60 * 64, 60 * 64 - 70, 64 * 5, 64]
+    m = S.make_method("linear", k_start=40.0, mu=0.3, k_min=2)
+    budget, kcap = S.stem_decode_budget(wide, m, DEV)
+    idx, cnt = S.stem_decode_select(gpu, q.to(DEV), i32(lens), budget, kcap, m, rows=i32([0] * 4))
+    most = math.ceil(40.0 * float(np.float32(0.3)))  # 13: the float 0.3 is above 0.3
+    assert cnt.cpu().tolist() == [[most] * 4, [most] * 4, [5] * 4, [1] * 4]
+    common.check_select(gpu, q, [0] * 4, lens, budget.tolist(), kb, vn, table, "head", "product", 0.0,
+                        True, idx, cnt, kcap)
