@@ -79,20 +79,23 @@ int cache_rows(bool write, const stem_cache_t* c, void* k, void* v, int dtype, i
   if (T < 0 || strides == nullptr) return STEM_ERR_ARG;
   if (static_cast<int64_t>(T) > static_cast<int64_t>(c->max_blocks) * c->block) return STEM_ERR_ARG;
   const int64_t elt = dtype == STEM_BF16 ? 2 : 4;
-  for (int n = 0; n < 3; ++n)
-    if (strides[n] < 0 || strides[n] * elt % 16 != 0) return STEM_ERR_ARG;
+  const int32_t extent[3] = {c->nseq, c->Hkv, T};
+  int64_t step[3];  // (along an axis of one row there is none, whatever its stride says)
+  for (int n = 0; n < 3; ++n) {
+    step[n] = extent[n] > 1 ? strides[n] : 0;
+    if (step[n] < 0 || step[n] * elt % 16 != 0) return STEM_ERR_ARG;
+  }
   if (c->nseq == 0 || T == 0) return STEM_OK;
   // (rows that are written need places of their own)
-  if (!write && ((c->nseq > 1 && strides[0] == 0) || (c->Hkv > 1 && strides[1] == 0) ||
-                 (T > 1 && strides[2] == 0)))
-    return STEM_ERR_ARG;
+  for (int n = 0; n < 3; ++n)
+    if (!write && extent[n] > 1 && step[n] == 0) return STEM_ERR_ARG;
   if ((rc = check_buffers(c)) != STEM_OK) return rc;
   if (!k || !v || !pos || !aligned(k, 16) || !aligned(v, 16) || !aligned(pos, 4) ||
       !aligned(count, 4) || !aligned(status, 4))
     return STEM_ERR_ARG;
   if ((rc = clear_status(status, st)) != STEM_OK) return rc;
   return cuda_err(launch_cache_rows(write, c->format, c->D, dtype, device_cache(c), k, v, T,
-                                    strides[0], strides[1], strides[2], pos, count, status, st));
+                                    step[0], step[1], step[2], pos, count, status, st));
 }
 
 // ------------------------------------------------------------------ decode

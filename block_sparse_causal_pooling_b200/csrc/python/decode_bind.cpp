@@ -217,8 +217,10 @@ PyObject* rows(bool write, PyObject* const* a, Py_ssize_t n) {
       fail(PyExc_ValueError, "k must be [" + std::to_string(s.nseq) + ", " +
                                  std::to_string(s.Hkv) + ", T, " + std::to_string(s.D) +
                                  "], got " + text(k.sizes()));
-    if (v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type() || v.strides() != k.strides())
-      fail(PyExc_ValueError, "k and v must have the same shape, dtype and strides");
+    bool alike = v.sizes() == k.sizes() && v.scalar_type() == k.scalar_type();
+    for (int64_t n = 0; alike && n < 4; ++n)  // (the stride of an axis of one row says nothing)
+      alike = k.size(n) == 1 || v.stride(n) == k.stride(n);
+    if (!alike) fail(PyExc_ValueError, "k and v must have the same shape, dtype and strides");
     if (k.device() != dev || v.device() != dev)
       fail(PyExc_ValueError, "k and v must be on the cache's device " + dev.str());
     if (k.stride(3) != 1)

@@ -434,7 +434,7 @@ size_t stem_cache_page_bytes(int D, int block, int format);
  * float32; element ((s * strides[0]) + (h * strides[1]) + (t * strides[2]) + d, d contiguous) becomes
  * token pos[s] + t of sequence s, for t < count[s] (NULL: T for every sequence). pos and count are
  * device int32[nseq], 0 <= count[s] <= T <= max_blocks * block. Strides are host values in elements,
- * not negative, and multiples of 16 bytes. Each block whose last token is written gets its
+ * not negative, and multiples of 16 bytes; that of an axis of one row is not used. Each block whose last token is written gets its
  * summaries; tokens of it that came earlier are read back from the page. Writing a position again replaces it, so a caller
  * may take tokens back by appending at an earlier position. Two sequences of one call must not
  * write the same page. status as in stem_args_t.

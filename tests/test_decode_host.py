@@ -1,10 +1,25 @@
 """The host side of the decode path on the CPU: budgets, argument checks and the build of the binding."""
 
+import json
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from block_sparse_causal_pooling_b200 import decode as D
 from block_sparse_causal_pooling_b200 import stem as S
+from tests import test_decode_abi as abi
+
+
+def abi_probe(code):
+    """What `code` prints (JSON) after the helpers of test_decode_abi.PROBE, in a process without a GPU."""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="", PYTHONPATH=abi.ROOT)
+    r = subprocess.run([sys.executable, "-c", abi.PROBE.split("out = {}")[0] + code], env=env,
+                       capture_output=True, text=True, timeout=300, cwd=abi.ROOT)
+    assert r.returncode == 0, r.stderr
+    return json.loads(r.stdout.strip().splitlines()[-1])
 
 
 @pytest.mark.parametrize("k_start,mu,k_min", [(20.0, 0.25, 2), (7.5, 0.9, 3), (300.0, 1.0, 1),
@@ -17,3 +32,23 @@ def test_the_linear_schedule_is_that_of_a_context_which_ends_here(k_start, mu, k
         want = [int(S.stem_budget_m(i + 1, m)[0][i]) for i in range(width)]
         assert budget.tolist() == want and budget.dtype == torch.int32
         assert kcap == max(want)
+
+
+def test_the_stride_of_an_axis_of_one_row_is_not_looked_at():
+    """It may be anything: unaligned, negative, 0; along an axis of several rows it is refused."""
+    got = abi_probe("""
+cases = {}
+for name in ("stem_cache_append", "stem_cache_read"):
+    for n in range(3):
+        for bad in (132, -128, 3):
+            st = [2048, 1024, 128]
+            st[n] = bad
+            one = dict(c=cache(nseq=1) if n == 0 else cache(Hkv=1) if n == 1 else cache(),
+                       T=1 if n == 2 else 4)
+            cases[f"{name} {n} {bad}"] = [rows(getattr(L, name), strides=st),
+                                          rows(getattr(L, name), strides=st, **one)]
+print(json.dumps(cases))
+""")
+    assert len(got) == 18
+    for case, (several, one) in got.items():
+        assert several == S.STEM_ERR_ARG and one != S.STEM_ERR_ARG, case

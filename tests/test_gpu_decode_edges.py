@@ -244,3 +244,39 @@ def test_select_with_the_linear_schedule(wide):
     assert cnt.cpu().tolist() == [[most] * 4, [most] * 4, [5] * 4, [1] * 4]
     common.check_select(gpu, q, [0] * 4, lens, budget.tolist(), kb, vn, table, "head", "product", 0.0,
                         True, idx, cnt, kcap)
+
+
+# ------------------------------------------------------------------ the cache
+
+
+@pytest.mark.parametrize("axis", [0, 1, 2])
+def test_rows_whose_strides_differ_along_an_axis_of_one(axis):
+    """K as it comes and V as a transposed view hold one layout where an axis has one row."""
+    g = torch.Generator().manual_seed(42)
+    shape = [2, 3, 4]
+    shape[axis] = 1
+    B, H, T = shape
+    D = 64
+    table, pages = common.make_table([1] * B, 1)
+    k, v = rows(g, B, H, T, D).to(DEV), rows(g, B, H, T, D).to(DEV)
+    step = list(v.stride())
+    step[axis] = {0: 3, 1: 7, 2: 5}[axis]
+    odd = torch.as_strided(v, v.shape, step)
+    assert torch.equal(odd, v) and odd.stride() != k.stride()
+    got = []
+    for vv in (v, odd):
+        gpu, _ = common.pair(pages, H, D, 64, "q8", table)
+        S.stem_cache_append(gpu, k, vv, i32([0] * B))
+        got.append(S.stem_cache_read(gpu, i32([0] * B), T=T))
+        into = [torch.as_strided(torch.zeros_like(v), v.shape, step), torch.zeros_like(v)]
+        S.stem_cache_read(gpu, i32([0] * B), k=into[0], v=into[1])
+        assert torch.equal(into[0], got[-1][0]) and torch.equal(into[1], got[-1][1])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    one = rows(g, 2, 3, 1, D).to(DEV)
+    turned = one.transpose(1, 2).contiguous().transpose(1, 2)  # [B, 1, H, D] seen as [B, H, 1, D]
+    table, pages = common.make_table([1, 1], 1)
+    gpu, cpu = common.pair(pages, 3, D, 64, "bf16", table)
+    S.stem_cache_append(gpu, one, turned, i32([0, 0]))
+    k2, v2 = S.stem_cache_read(gpu, i32([0, 0]), T=1)
+    assert torch.equal(k2, one) and torch.equal(v2, one)
