@@ -151,6 +151,13 @@ def stem_decode_workspace_size(cache: PagedCache, R: int, Hq: int, kcap: int) ->
     return _decode.workspace_size(cache, R, Hq, kcap)
 
 
+def _method(method) -> int:
+    """The address of method parameters, which the native part reads."""
+    if not isinstance(method, stem_method_t):
+        raise TypeError(f"method must be a stem_method_t (make_method), got {type(method).__name__}")
+    return ctypes.addressof(method)
+
+
 def _both(sel_idx, sel_cnt) -> None:
     if (sel_idx is None) != (sel_cnt is None):
         raise ValueError("give both of sel_idx and sel_cnt, or neither")
@@ -162,8 +169,9 @@ def stem_decode_select(cache: PagedCache, q, lens, budget, kcap: int, method: st
     (None: sequence r). Returns (sel_idx [R, Hq, kcap], ascending, -1 past the count, and sel_cnt
     [R, Hq])."""
     _both(sel_idx, sel_cnt)
-    return _decode.decode(_SELECT, cache, q, lens, rows, budget, kcap, ctypes.addressof(method),
-                          sel_idx, sel_cnt, None, None, None, status, _handle(cache, stream))[2:]
+    method = _method(method)
+    return _decode.decode(_SELECT, cache, q, lens, rows, budget, kcap, method, sel_idx, sel_cnt,
+                          None, None, None, status, _handle(cache, stream))[2:]
 
 
 def stem_decode_attn(cache: PagedCache, q, lens, sel_idx, sel_cnt, share: str = "head", rows=None,
@@ -177,7 +185,7 @@ def stem_decode_attn(cache: PagedCache, q, lens, sel_idx, sel_cnt, share: str = 
     if sel_idx.dim() != 3:
         raise ValueError(f"sel_idx must be [R, Hq, kcap], got {tuple(sel_idx.shape)}")
     return _decode.decode(_ATTEND, cache, q, lens, rows, None, sel_idx.shape[2],
-                          ctypes.addressof(_ATTN[share]), sel_idx, sel_cnt, out, lse, workspace,
+                          _method(_ATTN[share]), sel_idx, sel_cnt, out, lse, workspace,
                           status, _handle(cache, stream))[:2]
 
 
@@ -186,6 +194,6 @@ def stem_decode(cache: PagedCache, q, lens, budget, kcap: int, method: stem_meth
                 stream=None):
     """stem_decode_select and stem_decode_attn as one call: (out, lse, sel_idx, sel_cnt)."""
     _both(sel_idx, sel_cnt)
-    return _decode.decode(_SELECT | _ATTEND, cache, q, lens, rows, budget, kcap,
-                          ctypes.addressof(method), sel_idx, sel_cnt, out, lse, workspace, status,
-                          _handle(cache, stream))
+    method = _method(method)
+    return _decode.decode(_SELECT | _ATTEND, cache, q, lens, rows, budget, kcap, method, sel_idx,
+                          sel_cnt, out, lse, workspace, status, _handle(cache, stream))

@@ -1,5 +1,6 @@
 """The host side of the decode path on the CPU: budgets, argument checks and the build of the binding."""
 
+import ctypes
 import json
 import os
 import subprocess
@@ -52,3 +53,11 @@ print(json.dumps(cases))
     assert len(got) == 18
     for case, (several, one) in got.items():
         assert several == S.STEM_ERR_ARG and one != S.STEM_ERR_ARG, case
+
+
+def test_method_parameters_are_of_their_type():
+    """Their memory is read by address: nothing else may stand in for them, above all nothing smaller."""
+    for method in (ctypes.c_int32(0), S.stem_cache_t(), None, "exp", 0):
+        for call in (D.stem_decode_select, D.stem_decode):
+            with pytest.raises(TypeError, match="stem_method_t"):
+                call(None, None, None, None, 1, method)
