@@ -23,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libstem.so")
 BIND = os.path.join(PKG, "_decode.so")
+STAMP = os.path.join(BUILD, "_decode.stamp")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -67,13 +68,11 @@ def _compile(src: str, verbose: bool) -> tuple[str, str]:
 
 
 def _build_binding(force: bool) -> None:
-    src = os.path.join(CSRC, "python", "decode_bind.cpp")
-    if not force and not _stale(BIND, [src, os.path.join(INCLUDE, "stem.h"), LIB]):
-        return
     import sysconfig
 
     import torch
 
+    src = os.path.join(CSRC, "python", "decode_bind.cpp")
     troot = os.path.dirname(os.path.abspath(torch.__file__))
     tinc, tlib = os.path.join(troot, "include"), os.path.join(troot, "lib")
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
@@ -87,10 +86,22 @@ def _build_binding(force: bool) -> None:
         cmd += ["-I", i]
     cmd += ["-o", tmp, src, "-L", PKG, "-l:libstem.so", "-L", tlib, "-ltorch_python", "-ltorch",
             "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    # what the module was made with and for, wherever the tree lies: another torch or Python has another
+    # binary interface
+    stamp = "\n".join([torch.__version__, sys.version] + [c.replace(ROOT, "") for c in cmd])
+    made = ""
+    if os.path.exists(STAMP):
+        with open(STAMP) as f:
+            made = f.read()
+    if not force and made == stamp and not _stale(BIND, [src, os.path.join(INCLUDE, "stem.h"), LIB]):
+        return
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for decode_bind.cpp:\n" + r.stderr)
     os.replace(tmp, BIND)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(STAMP, "w") as f:
+        f.write(stamp)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

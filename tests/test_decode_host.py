@@ -9,6 +9,7 @@ import sys
 import pytest
 import torch
 
+from block_sparse_causal_pooling_b200 import build as libbuild
 from block_sparse_causal_pooling_b200 import decode as D
 from block_sparse_causal_pooling_b200 import stem as S
 from tests import test_decode_abi as abi
@@ -61,3 +62,32 @@ def test_method_parameters_are_of_their_type():
         for call in (D.stem_decode_select, D.stem_decode):
             with pytest.raises(TypeError, match="stem_method_t"):
                 call(None, None, None, None, 1, method)
+
+
+def test_the_binding_is_built_again_for_another_torch_python_or_command(monkeypatch, tmp_path):
+    ran = []
+
+    def gxx(cmd, **kw):
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    for name, at in (("BIND", "_decode.so"), ("STAMP", "stamp"), ("BUILD", "build")):
+        monkeypatch.setattr(libbuild, name, str(tmp_path / at))
+    monkeypatch.setattr(libbuild.subprocess, "run", gxx)
+
+    def builds():
+        n = len(ran)
+        libbuild._build_binding(False)
+        return len(ran) - n
+
+    assert builds() == 1 and os.path.exists(libbuild.BIND)
+    assert builds() == 0
+    os.remove(libbuild.STAMP)
+    assert builds() == 1 and builds() == 0
+    for change in ((torch, "__version__", "0.0"), (sys, "version", "0.0"),
+                   (libbuild, "INCLUDE", libbuild.INCLUDE + "/")):
+        monkeypatch.setattr(*change)
+        assert builds() == 1 and builds() == 0, change[1]
+    monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
+    assert builds() == 1 and builds() == 0
