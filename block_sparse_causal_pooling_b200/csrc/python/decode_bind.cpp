@@ -278,6 +278,9 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count_is(n, 15)) return nullptr;
   try {
     const int64_t what = integer(a[0]);
+    const char* name = what == kSelect   ? "stem_decode_select"
+                       : what == kAttend ? "stem_decode_attn"
+                                         : "stem_decode";
     const Cache& c = cache_of(a[1]);
     const stem_cache_t& s = c.c;
     const at::Device dev = device_of(c);
@@ -287,6 +290,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t R = q.size(0), Hq = q.size(1), kcap = integer(a[6]);
     need(q, "q", at::kBFloat16, q.sizes(), dev);
     if (kcap < 1) fail(PyExc_ValueError, "kcap must be at least 1");
+    if (kcap > s.max_blocks) check_rc(STEM_ERR_ARG, name);  // (before lists of that size are made)
     stem_decode_args_t d = {};
     d.cache = &s;
     d.q = q.data_ptr();
@@ -330,8 +334,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     rc = what == kSelect ? stem_decode_select(&d, st)
                          : what == kAttend ? stem_decode_attn(&d, st) : stem_decode(&d, st);
     Py_END_ALLOW_THREADS
-    check_rc(rc, what == kSelect ? "stem_decode_select"
-                                 : what == kAttend ? "stem_decode_attn" : "stem_decode");
+    check_rc(rc, name);
     // given tensors go back as the objects they came as
     auto back = [](PyObject* given, const at::Tensor& t) {
       if (given != Py_None || !t.defined()) return Py_NewRef(given);

@@ -280,3 +280,20 @@ def test_rows_whose_strides_differ_along_an_axis_of_one(axis):
     S.stem_cache_append(gpu, one, turned, i32([0, 0]))
     k2, v2 = S.stem_cache_read(gpu, i32([0, 0]), T=1)
     assert torch.equal(k2, one) and torch.equal(v2, one)
+
+
+def test_a_list_longer_than_the_table_is_refused_before_it_is_made():
+    """kcap above max_blocks is an invalid argument, not an allocation of that size."""
+    g = torch.Generator().manual_seed(43)
+    gpu, _ = common.filled("q8", 64, 64, 2, [300, 64], g)
+    m = S.make_method("exp", rho_min=0.3, tau=3.0, k_min=2)
+    budget, _ = S.stem_decode_budget(gpu.max_blocks, m, DEV)
+    q, lens = rows(g, 2, 4, 64).to(DEV), i32([300, 64])
+    for call in (S.stem_decode_select, S.stem_decode):
+        for kcap in (gpu.max_blocks + 1, 1 << 24, 1 << 40):
+            torch.cuda.synchronize()
+            torch.cuda.reset_peak_memory_stats()
+            before = torch.cuda.memory_allocated()
+            with pytest.raises(S.StemError, match="invalid argument"):
+                call(gpu, q, lens, budget, kcap, m)
+            assert torch.cuda.max_memory_allocated() == before
