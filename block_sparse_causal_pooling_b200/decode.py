@@ -109,8 +109,9 @@ def _handle(cache: PagedCache, stream):
 def stem_cache_append(cache: PagedCache, k, v, pos, count=None, status=None, stream=None) -> None:
     """Write K and V rows k, v [nseq, Hkv, T, D] (bf16 or f32, any strides with a contiguous last
     dimension and rows on 16-byte boundaries) as tokens pos[s] .. pos[s] + count[s] - 1 of each
-    sequence (count None: all T), quantised to the cache's format, and summarise the blocks that
-    this completes."""
+    sequence (count None: all T), quantised to the cache's format, and summarise the blocks whose
+    last token is among them. A token written again in the middle of a full block leaves the block's
+    summaries as they were: write on to its end to renew them."""
     _decode.append(cache, k, v, pos, count, status, _handle(cache, stream))
 
 

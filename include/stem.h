@@ -435,8 +435,10 @@ size_t stem_cache_page_bytes(int D, int block, int format);
  * token pos[s] + t of sequence s, for t < count[s] (NULL: T for every sequence). pos and count are
  * device int32[nseq], 0 <= count[s] <= T <= max_blocks * block. Strides are host values in elements,
  * not negative, and multiples of 16 bytes; that of an axis of one row is not used. Each block whose last token is written gets its
- * summaries; tokens of it that came earlier are read back from the page. Writing a position again replaces it, so a caller
- * may take tokens back by appending at an earlier position. Two sequences of one call must not
+ * summaries; tokens of it that came earlier are read back from the page. Writing a position again
+ * replaces it, so a caller may take tokens back by appending at an earlier position. The summaries of
+ * a full block stay those of its former tokens until its last token is written again too: a token in
+ * its middle is changed by writing from there to the block's end. Two sequences of one call must not
  * write the same page. status as in stem_args_t.
  */
 int stem_cache_append(const stem_cache_t* c, const void* k, const void* v, int dtype, int T,

@@ -297,3 +297,26 @@ def test_a_list_longer_than_the_table_is_refused_before_it_is_made():
             with pytest.raises(S.StemError, match="invalid argument"):
                 call(gpu, q, lens, budget, kcap, m)
             assert torch.cuda.max_memory_allocated() == before
+
+
+@pytest.mark.parametrize("fmt", common.FORMATS)
+def test_summaries_follow_the_last_token_of_a_block(fmt):
+    """A token written again in the middle of a full block changes the token alone; written on to the
+    block's end, the summaries are those of the block as it stands."""
+    g = torch.Generator().manual_seed(44)
+    D, block, n = 64, 64, 128
+    k, v = rows(g, 1, 1, n, D).to(DEV), rows(g, 1, 1, n, D).to(DEV)
+    new = rows(g, 1, 1, n, D).to(DEV)
+    table, pages = common.make_table([2], 2)
+    gpu, _ = common.pair(pages, 1, D, block, fmt, table)
+    S.stem_cache_append(gpu, k, v, i32([0]))
+    kbar, vnorm = gpu.kbar.clone(), gpu.vnorm.clone()
+    S.stem_cache_append(gpu, new[:, :, 30:31], new[:, :, 30:31], i32([30]))
+    assert torch.equal(gpu.kbar, kbar) and torch.equal(gpu.vnorm, vnorm)
+    S.stem_cache_append(gpu, k[:, :, 31:64], v[:, :, 31:64], i32([31]))
+    fresh, _ = common.pair(pages, 1, D, block, fmt, table)
+    k[:, :, 30], v[:, :, 30] = new[:, :, 30], new[:, :, 30]
+    S.stem_cache_append(fresh, k, v, i32([0]))
+    assert torch.equal(gpu.pages, fresh.pages)
+    assert torch.equal(gpu.kbar, fresh.kbar) and torch.equal(gpu.vnorm, fresh.vnorm)
+    assert not torch.equal(gpu.kbar, kbar)
