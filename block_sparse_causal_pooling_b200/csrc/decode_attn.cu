@@ -64,11 +64,15 @@ constexpr int kStaged = 128;  // list entries in shared memory at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A logit may exceed the running maximum by this much (in log2 units) before the accumulators are
-// rescaled: weights stay below 2^5, and most steps need neither the warp's maximum nor a rescale.
-constexpr float kSlack = 5.f;
-// The V scales' power of two puts the largest scale in [2^6, 2^7) when it is set, and is set again
-// when a scale exceeds 2^10 in its units: weights stay below 2^15, fp16's range.
-constexpr int kScaleSet = 6, kScaleSlack = 3;
+// rescaled: weights stay below 2^4, and most steps need neither the warp's maximum nor a rescale.
+constexpr float kSlack = 4.f;
+// The V scales' power of two puts the largest scale in [2^8, 2^9) when it is set, and is set again
+// when a scale exceeds 2^11 in its units: weights stay below 2^15, fp16's range. The narrower the
+// slacks, the more often both are set again, and the fewer entries are gone over again. (Slacks of 2^5 and
+// scales from 2^6: every block of 32 sequences of 64K at 8 bits, weights all on one token, 1310 us where
+// these take 703 and weights on many 693. 2^3 and 2^10: 695, but 64 ragged rows of up to 32K 91.6
+// instead of 90.6.)
+constexpr int kScaleSet = 8, kScaleSlack = 2;
 // A sum of weights that n tokens may be off by 2^-12 of, at 2^-25 each, is below n times this.
 constexpr float kLeastSum = 0x1p-13f;
 
@@ -972,7 +976,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D>::THREADS, Cfg<FMT, D>::CTAS) attn_
           f0[y] = fmaxf(f0[y], __shfl_xor_sync(kFull, f0[y], o));
           f1[y] = fmaxf(f1[y], __shfl_xor_sync(kFull, f1[y], o));
         }
-        // the largest weight to [2^14, 2^15), or below where it is infinite (less than 2^(5 + 126)) or
+        // the largest weight to [2^14, 2^15), or below where it is infinite (less than 2^(4 + 126)) or
         // next to nothing
         auto power = [](float w) {
           const int up = 14 + 127 - static_cast<int>(__float_as_uint(w) >> 23);
