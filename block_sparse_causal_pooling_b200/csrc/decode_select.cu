@@ -329,7 +329,6 @@ static_assert(below_most(1), "kMaxSmem is the most");
 // CTAS: CTAs of an SM that the registers are shared out for, 2 or 4 (see launch_decode_select).
 template <int D, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) select_kernel(const Args a) {
-  constexpr int NI = D / 32;  // float4 of a lane and block
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Sums s;
   __shared__ Teams team;
@@ -465,9 +464,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) select_kernel(const Args a) {
           if (!(top > -INFINITY)) top = 0.0;
           for (int c = 0; c < csize; ++c) {
             // a CTA without a finite score (of a short row, say) has no part in it: its sum is 0 (or
-            // NaN), and exp(-top) may be infinite
-            const double there = s.top[c][tid];
-            sum += there > -INFINITY ? s.sum[c][tid] * exp(there - top) : s.sum[c][tid];
+            // NaN), and exp(-top) might be infinite (a choice of exponents, not a branch around exp,
+            // which would run the CTAs' one after the other)
+            const double base = s.top[c][tid] > -INFINITY ? s.top[c][tid] : top;
+            sum += s.sum[c][tid] * exp(base - top);
           }
           s.lse[tid] = top + log(sum);
         }
