@@ -12,10 +12,12 @@
 // a block came at once or token by token, and writing a position again gives what writing it once
 // gives.
 //
-// Bound: HBM (rows in, codes out). Measured (B200, device time in a graph; the first two written and
-// read back): a 128K prompt at 16 bits, 8 kv heads of 128, 356 us of 250 at a copy's rate; 8 ragged
-// chunks of up to 1999 tokens at 8 bits 23 us of 6.8; reading 32K at 4 bits 30 us of 26.6. One CTA per (block, kv head, sequence); a thread holds the same
-// 8 channels of a token pair of every tile.
+// Bound: HBM (rows in, codes out). Measured (B200, device time in a graph, against the bytes at a copy's
+// rate): writing a 128K prompt, 8 kv heads of 128, 195 us of 166 at 16 bits, 242 of 127 at 8 and 228 of
+// 106 at 4, where packing the codes stands between a tile's loads and the next; 8 ragged chunks of up to
+// 1999 tokens at 8 bits, 2 heads of 64, 15 us of 4, a chain of loads for little work a CTA. Reading the same:
+// 161, 128 and 108 us, and 7. One token of 16 sequences at 4 bits 5.8 and 2.2 us. One CTA per (block, kv
+// head, sequence); a thread holds the same 8 channels of a token pair of every tile.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -335,8 +337,8 @@ constexpr int kThreads = 256;
 constexpr int kAppendCtas = 3;
 
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(KvCache c_, Rows r, const T* k,
-                                                          const T* v) {
+__global__ void __launch_bounds__(kThreads, kAppendCtas)
+    append_kernel(KvCache c_, Rows r, const T* k, const T* v) {
   using L = Kv<FMT, D>;
   constexpr int CH = D / 8;                    // chunks of a row
   constexpr int SLOTS = kThreads / (8 * CH);  // tiles at a time

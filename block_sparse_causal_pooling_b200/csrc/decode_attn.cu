@@ -35,8 +35,8 @@
 // sums are float32. Warps, then CTAs of one (row, kv head), are joined by (max, sum, numerator).
 //
 // Measured (B200; 16 sequences, 32 heads on 8 kv heads of 128, every block; device time in a graph),
-// at 4K, 8K, 16K and 32K tokens: 16 bits 56, 95, 175 and 331 us, 8 bits 41, 63, 108 and 197 us, 4 bits
-// 33, 49, 81 and 144 us; at 32K 6.5, 5.8 and 4.2 TB/s (a copy reaches 6.47). A line through the four
+// at 4K, 8K, 16K and 32K tokens: 16 bits 56, 95, 176 and 334 us, 8 bits 40, 62, 108 and 196 us, 4 bits
+// 34, 50, 81 and 145 us; at 32K 6.4, 5.8 and 4.2 TB/s (a copy reaches 6.47). A line through the four
 // has a slope of 6.8, 6.4 and 4.8 TB/s and starts at 17 to 18 us. Few rows are bound by latency, long
 // lists at 16 and 8 bits by HBM, at 4 bits by the instructions that unpack and scale.
 #include <cuda_bf16.h>
@@ -54,8 +54,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kHeadTile = kDecodeHeads;
-// Steps of a CTA below which an item is not split further: two a warp. (A short context, 10 blocks:
-// 12.7 us with 8 steps a CTA, 13.6 with 16; one row over 52 blocks: 14.8 and 14.7.)
+// Steps of a CTA below which an item is not split further: two a warp. (A selection and its attention of
+// one row of 16 blocks of 64 at 16 bits: 13.1 us with 8 steps a CTA, 13.3 with 16; one row over 52 blocks
+// of 128 at 4 bits: 13.4 and 13.1.)
 constexpr int kMinSteps = 8;
 // Items in parts are joined by the CTA that brings the last part, which saves a launch, unless they
 // have more parts than this on average: then by a kernel of their own, with a CTA for each head.

@@ -7,8 +7,8 @@ namespace stem {
 
 // A launch that may be set up while the stream's previous kernel still runs: the kernel waits for it
 // itself (cudaGridDependencySynchronize) before it touches memory. Such a launch also costs the host
-// 2 us where a plain one costs 3.8. cluster: CTAs of a cluster along
-// x; 1 launches without clusters.
+// 2.4 us where a plain one costs 2.9 (200 in a row of a kernel with 256 bytes of arguments). cluster: CTAs
+// of a cluster along x; 1 launches without clusters.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
                          cudaStream_t st, const A&... args) {

@@ -16,7 +16,7 @@
 // heads' softmax sums and then the keys are exchanged through distributed shared memory, and each
 // list is picked by one CTA of the cluster.
 //
-// Measured (B200, device time in a graph): one row at the end of 128K tokens (32 heads on 8) 12.3 us,
+// Measured (B200, device time in a graph): one row at the end of 128K tokens (32 heads on 8) 12.4 us,
 // where reading kbar takes 0.65; 32 ragged rows of up to 64K (28 heads on 4, blocks of 64) 33 us of
 // 5.7. Neither is near the floor: what is left is a chain of exchanges and exact ranking, not bytes.
 #include <cooperative_groups.h>

@@ -434,12 +434,12 @@ size_t stem_cache_page_bytes(int D, int block, int format);
  * float32; element ((s * strides[0]) + (h * strides[1]) + (t * strides[2]) + d, d contiguous) becomes
  * token pos[s] + t of sequence s, for t < count[s] (NULL: T for every sequence). pos and count are
  * device int32[nseq], 0 <= count[s] <= T <= max_blocks * block. Strides are host values in elements,
- * not negative, and multiples of 16 bytes; that of an axis of one row is not used. Each block whose last token is written gets its
- * summaries; tokens of it that came earlier are read back from the page. Writing a position again
- * replaces it, so a caller may take tokens back by appending at an earlier position. The summaries of
- * a full block stay those of its former tokens until its last token is written again too: a token in
- * its middle is changed by writing from there to the block's end. Two sequences of one call must not
- * write the same page. status as in stem_args_t.
+ * not negative, and multiples of 16 bytes; that of an axis of one row is not used. Each block whose
+ * last token is written gets its summaries; tokens of it that came earlier are read back from the
+ * page. Writing a position again replaces it, so a caller may take tokens back by appending at an
+ * earlier position. The summaries of a full block stay those of its former tokens until its last
+ * token is written again too: a token in its middle is changed by writing from there to the block's
+ * end. Two sequences of one call must not write the same page. status as in stem_args_t.
  */
 int stem_cache_append(const stem_cache_t* c, const void* k, const void* v, int dtype, int T,
                       const int64_t* strides, const int32_t* pos, const int32_t* count,
@@ -456,7 +456,9 @@ int stem_cache_read(const stem_cache_t* c, void* k, void* v, int dtype, int T,
  * Arguments of a decode step: R query tokens ("rows"), each of one sequence of the cache. Several
  * rows may belong to one sequence (draft tokens), each with its own number of visible tokens.
  *   q [R, Hq, D], out [R, Hq, D]  bfloat16 (dtype STEM_F32 returns STEM_ERR_UNSUPPORTED); at 8
- *                                 and 4 bits, |q| < 2^115 (its scaling to fp16 ends there)
+ *                                 and 4 bits, |q| < 2^115 (its scaling to fp16 ends there), and
+ *                                 entries below 2^-27 of a head's largest are rounded, by up to
+ *                                 2^-35 of that
  *   lse [R, Hq] float32           optional: ln of the softmax denominator
  *   rows [R] int32                sequence of each row; NULL: row r is sequence r (R <= nseq)
  *   lens [R] int32                tokens that the row sees: 0 .. len - 1, its own K and V (appended
@@ -497,7 +499,9 @@ size_t stem_decode_workspace_size(const stem_cache_t* c, int R, int Hq, int kcap
  * The blocks each row keeps. With i = ceil(len / block) - 1 the row's own (diagonal) block and
  * k = budget[i] (2 <= k <= i + 1 for i >= 1, 1 at i = 0):
  *   s_hj = q_h . kbar_j / sqrt(D), j < i;  product: s_hj + ln n_j;  additive: s_hj + beta e_j
- *   group share: ln n_j + ln sum_h softmax_{j < i}(s_h)_j, or sum_h s_hj + G beta e_j
+ *   group share: ln n_j + ln sum_h softmax_{j < i}(s_h)_j, or sum_h s_hj + G beta e_j (the prefill's
+ *   softmax is over j <= i; here the diagonal block, kept in any case, has no part in it, as it need
+ *   not have a summary: a head that looks at it alone counts in full among the blocks before)
  *   kept = {0, i} and the k - 2 best of 1 .. i - 1, ties to the lower block; a key that is NaN
  *   ranks last.
  * Scores, metric and comparisons are double. out and lse are not used.
