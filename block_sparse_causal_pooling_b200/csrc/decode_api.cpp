@@ -2,6 +2,7 @@
 // launch sequence for the paged cache and the attention of single query tokens.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -70,6 +71,21 @@ int clear_status(int32_t* status, cudaStream_t st) {
   return status ? cuda_err(cudaMemsetAsync(status, 0, sizeof(int32_t), st)) : STEM_OK;
 }
 
+// Rows that are written need places of their own: each step, from the smallest on, leaves what the
+// smaller ones span behind it.
+bool apart(const int64_t* step, const int32_t* extent, int D) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return step[a] < step[b]; });
+  int64_t span = D;
+  for (const int n : order) {
+    if (extent[n] < 2) continue;
+    if (step[n] < span) return false;
+    if (step[n] > (INT64_MAX - span) / (extent[n] - 1)) return false;  // (past any memory)
+    span += step[n] * (extent[n] - 1);
+  }
+  return true;
+}
+
 int cache_rows(bool write, const stem_cache_t* c, void* k, void* v, int dtype, int T,
                const int64_t* strides, const int32_t* pos, const int32_t* count, int32_t* status,
                cudaStream_t st) {
@@ -86,9 +102,7 @@ int cache_rows(bool write, const stem_cache_t* c, void* k, void* v, int dtype, i
     if (step[n] < 0 || step[n] * elt % 16 != 0) return STEM_ERR_ARG;
   }
   if (c->nseq == 0 || T == 0) return STEM_OK;
-  // (rows that are written need places of their own)
-  for (int n = 0; n < 3; ++n)
-    if (!write && extent[n] > 1 && step[n] == 0) return STEM_ERR_ARG;
+  if (!write && !apart(step, extent, c->D)) return STEM_ERR_ARG;
   if ((rc = check_buffers(c)) != STEM_OK) return rc;
   if (!k || !v || !pos || !aligned(k, 16) || !aligned(v, 16) || !aligned(pos, 4) ||
       !aligned(count, 4) || !aligned(status, 4))

@@ -446,8 +446,8 @@ int stem_cache_append(const stem_cache_t* c, const void* k, const void* v, int d
                       int32_t* status, void* stream);
 
 /* The values that tokens pos[s] .. pos[s] + count[s] - 1 stand for, into k and v (rounded to
- * bfloat16, or exact in float32). Arguments as for stem_cache_append, but no stride may be 0 along
- * an axis of several rows; rows t >= count[s] are left as they were. */
+ * bfloat16, or exact in float32). Arguments as for stem_cache_append, but rows may not overlap (sorted,
+ * each stride is at least what the smaller ones span); rows t >= count[s] are left as they were. */
 int stem_cache_read(const stem_cache_t* c, void* k, void* v, int dtype, int T,
                     const int64_t* strides, const int32_t* pos, const int32_t* count,
                     int32_t* status, void* stream);

@@ -91,3 +91,21 @@ def test_the_binding_is_built_again_for_another_torch_python_or_command(monkeypa
         assert builds() == 1 and builds() == 0, change[1]
     monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
     assert builds() == 1 and builds() == 0
+
+
+def test_rows_read_back_may_not_overlap():
+    got = abi_probe("""
+read, append = L.stem_cache_read, L.stem_cache_append
+c = lambda **kw: cache(nseq=3, Hkv=2, D=64, **kw)
+cases = {}
+# T = 4 rows of 64, element strides of (sequence, head, token)
+for ok, st in ((1, (512, 256, 64)), (1, (512, 64, 128)), (1, (64, 1024, 192)), (1, (4096, 2048, 72)),
+               (0, (512, 256, 56)), (0, (512, 248, 64)), (0, (504, 256, 64)), (0, (512, 64, 64)),
+               (0, (64, 64, 64)), (0, (128, 256, 64)), (0, (512, 256, 8)), (0, (0, 256, 64)),
+               (0, (1 << 62, 256, 64)), (1, (1 << 40, 256, 64))):
+    cases[f"{ok} {st}"] = [rows(read, c(), strides=st), rows(append, c(), strides=st)]
+print(json.dumps(cases))
+""")
+    for case, (read, append) in got.items():
+        assert (read == S.STEM_ERR_ARG) == (case[0] == "0"), case
+        assert append != S.STEM_ERR_ARG, case  # (rows that are read may)
