@@ -9,7 +9,7 @@ A page holds one selection block of one sequence; the caller hands pages out by 
 [nseq, max_blocks]. Calls are asynchronous on `stream` (default: torch's current stream of the
 cache's device) and make that device current while they launch. Tensors that a call makes itself
 (outputs, workspace) are made for that stream, as under torch.cuda.stream(stream); a caller that
-reads them on another stream orders the two.
+reads them on another stream orders the two. The calls have no gradients: outputs do not require any.
 """
 
 from __future__ import annotations
